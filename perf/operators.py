@@ -227,7 +227,7 @@ def prepare(case, seed):
                                      weight_decay=st["weight_decay"], grad_scale=st["grad_scale"],
                                      max_norm=st["max_norm"], seed=st["seed"], loss_scaler=st["scaler"],
                                      grad_sumsq=st["sumsq"] if case["clip"] else None, lr_factor=st["lr_factor"],
-                                     decay=st["decay"], norm_out=st["norm_out"])
+                                     decay=st["decay"], norm_out=st["norm_out"] if case["clip"] else None)
     return st
 
 
