@@ -449,6 +449,129 @@ zero_status zero_loss_scaler_init(const zero_loss_scaler* cfg, zero_loss_scaler*
  * Errors: ZERO_EINVAL for NULL or misaligned pointers. */
 zero_status zero_loss_scaler_update(const int32_t* d_flag, zero_loss_scaler* d_scaler, void* stream);
 
+/* ------------------------------------------------------- AdamW, 32-bit and 8-bit states ------ */
+/* AdamW over rank r's shard: the Adam step above with decoupled weight decay [Loshchilov and
+ * Hutter, "Decoupled Weight Decay Regularization"], clipping by the global gradient norm, a rate
+ * that a captured graph can change, and a choice of states.  Not on the pages, which name Adam's
+ * states only; it is the step that large language models are trained with.  Per step, unfused:
+ *   zero_reduce_shard per bucket; zero_grad_sumsq if the norm is clipped (the ranks add their
+ *   sums: an all-reduce of one double); zero_adamw_step or zero_adamw8_step;
+ * fused: zero_pack_bucket_check per bucket; zero_adamw_prepare; zero_reduce_adamw_bucket or
+ * zero_reduce_adamw8_bucket per bucket.
+ *
+ * Workspace: the calls below that take d_work use zero_adamw_sizes.work_bytes bytes of device
+ * memory, 16-byte aligned, owned by the caller, its contents irrelevant before a step.  Calls that
+ * may run at the same time (on different streams, or in graphs replayed side by side) need
+ * different workspaces; a step's calls must name the same one.  With that, and with disjoint
+ * outputs, steps on one plan may overlap: the plan itself is not written. */
+typedef struct zero_adamw_sizes {
+    int64_t work_bytes;   /* bytes of d_work                                              */
+    int64_t n_scales;     /* pairs of scale bytes of 8-bit states: 2 * n_scales bytes     */
+} zero_adamw_sizes;
+
+/* Errors: ZERO_EINVAL for NULL arguments. */
+zero_status zero_adamw_get_sizes(const zero_plan* plan, zero_adamw_sizes* out);
+
+/* AdamW hyperparameters; host struct, read during the call, its pointers are device memory that
+ * the kernels read when they run.  With mult = grad_scale (/ loss_scaler->scale if given):
+ *   norm = sqrt(*grad_sumsq) * |mult|,  coef = max_norm > 0 ? min(1, max_norm / (norm + 1e-6)) : 1,
+ *   s = mult * coef (coef 1 without grad_sumsq; NaN if the norm is not finite, so that without
+ *   a flag the parameters show it),  lr = hp.lr * *lr_factor,  d_i = decay[i] (1 without decay).
+ * All in double, rounded to fp32 once. */
+typedef struct zero_adamw_hparams {
+    double lr;                            /* >= 0                                          */
+    double beta1, beta2;                  /* in [0, 1)                                     */
+    double eps;                           /* > 0 in fp32                                   */
+    double weight_decay;                  /* >= 0                                          */
+    double grad_scale;                    /* as zero_adam_hparams                          */
+    double max_norm;                      /* >= 0; 0 = no clipping; > 0 needs grad_sumsq   */
+    uint64_t seed;                        /* of the 8-bit states' rounding                 */
+    const zero_loss_scaler* loss_scaler;  /* device or NULL                                */
+    const double* grad_sumsq;             /* device or NULL: sum of squares over all ranks */
+    const float* lr_factor;               /* device or NULL: the schedule's factor         */
+    const float* decay;                   /* device float[n_params] or NULL                */
+    float* norm_out;                      /* device float[2] or NULL: norm and coef are written
+                                             (not on a skipped step); needs grad_sumsq     */
+} zero_adamw_hparams;
+
+/* *d_sumsq = the sum of g^2 over every element g of the live parameters' slices of d_g32, in
+ * double (exact squares; the sum is finite exactly when every g is), added in a fixed order: the
+ * result depends on the inputs alone.  If d_flag is not NULL, also ORs 1 into *d_flag when the sum
+ * is not finite: the check of zero_overflow_check in the same pass.
+ *   d_sumsq   device double[1], 8-byte aligned
+ * Errors: ZERO_EINVAL for NULL or misaligned pointers. */
+zero_status zero_grad_sumsq(const zero_plan* plan, const float* d_g32, const uint8_t* d_live, double* d_sumsq,
+                            int32_t* d_flag, void* d_work, void* stream);
+
+/* The first launch of the steps below: if d_flag is NULL or *d_flag == 0, every live parameter's
+ * step count advances and the step's scalars are formed in d_work; if the flag is set, nothing
+ * changes.  Only the fused path calls it by itself.
+ * Errors: ZERO_EINVAL for NULL or misaligned pointers or hyperparameters out of range. */
+zero_status zero_adamw_prepare(const zero_plan* plan, const uint8_t* d_live, int32_t* d_steps,
+                               const zero_adamw_hparams* hp, const int32_t* d_flag, void* d_work, void* stream);
+
+/* One AdamW step with 32-bit states.  As zero_adam_step, with for every element e of a live
+ * parameter i, t = d_steps[i] after the increment (fp32 arithmetic):
+ *     g = g32[e] * s ;  m = beta1*m + (1-beta1)*g ;  v = beta2*v + (1-beta2)*g*g
+ *     p32 -= lr * weight_decay * d_i * p32
+ *     p32 -= (lr / (1-beta1^t)) * m / (sqrt(v) / sqrt(1-beta2^t) + eps)
+ *     arena[Nd*O_b + r*L_b + (e - O_b)] = round_to_nearest_even_16(p32)
+ * Without decay, clipping and lr_factor the results are bit-identical to zero_adam_step's.
+ * Arguments and errors as zero_adam_step, and those of zero_adamw_prepare. */
+zero_status zero_adamw_step(const zero_plan* plan, const float* d_g32, float* d_p32, float* d_m, float* d_v,
+                            const uint8_t* d_live, int32_t* d_steps, const zero_adamw_hparams* hp,
+                            const int32_t* d_flag, void* d_arena, void* d_work, void* stream);
+
+/* The same step with 8-bit states: the momentum m and the root r of the variance (v = r^2), each
+ * a code times a power of two.  A block is the part of one parameter inside one aligned run of
+ * 256 shard columns; the block of column x and parameter i has its two scale bytes, m's first, at
+ * d_scales[2 * ((x >> 8) + i)], and scale byte k stands for 2^(k - 127).
+ *   m: OCP e4m3 (sign, 4 exponent bits of bias 7, 3 fraction bits; 448 the largest, no NaN);
+ *   r: 4 exponent bits of bias 15 and 4 fraction bits, no sign; exponent 0 holds subnormals:
+ *      code c stands for (c & 15) 2^-18 if c < 16, else (1 + (c & 15) / 16) 2^((c >> 4) - 15).
+ * States of zero bytes are zero.  A step decodes m and r, takes m, v = r^2 and p32 as above (each
+ * product and sum of m and v rounded to fp32 by itself), writes p32 and the 16-bit parameter from
+ * the unrounded new m and sqrt(v), gives every block of a live parameter the least scale under which
+ * its largest |m| (r) is at most 448 (1.9375), but at least 2^-111 (2^-95), and rounds m and r to
+ * the code below or above with a chance that keeps the mean; an r above zero never becomes zero.
+ * The chance is decided by a hash of hp->seed, the rank, t and the element's shard column: equal
+ * inputs give equal bits.  A block whose new m (r) is not finite everywhere gets scale byte 255
+ * and codes 0, and all of it reads as NaN from then on.  States of dead parameters, row gaps and
+ * skipped steps stay as they were.  Each state element takes 2 bytes and 1/64 instead of 8.
+ *   d_m8, d_r8   device uint8[shard_numel], 16-byte aligned
+ *   d_scales     device uint8[2 * n_scales], 16-byte aligned; entries that no block has are not used
+ * Other arguments and errors as zero_adamw_step. */
+zero_status zero_adamw8_step(const zero_plan* plan, const float* d_g32, float* d_p32, uint8_t* d_m8, uint8_t* d_r8,
+                             uint8_t* d_scales, const uint8_t* d_live, int32_t* d_steps,
+                             const zero_adamw_hparams* hp, const int32_t* d_flag, void* d_arena, void* d_work,
+                             void* stream);
+
+/* 8-bit states from 32-bit ones (d_m, d_v float[shard_numel]), of every parameter, live or not:
+ * scales as above, codes to the nearest, ties to the even code (a v above zero never becomes zero).
+ * v below zero reads as NaN.  Row gaps are not touched.  Errors: ZERO_EINVAL as zero_adamw8_step. */
+zero_status zero_adamw8_load(const zero_plan* plan, const float* d_m, const float* d_v, uint8_t* d_m8, uint8_t* d_r8,
+                             uint8_t* d_scales, void* stream);
+
+/* The values that 8-bit states stand for, m and r (not v), in bf16, which holds them exactly, of
+ * every parameter, live or not.  Row gaps are not touched.
+ *   d_m16, d_r16   device bf16[shard_numel], 16-byte aligned
+ * Errors: ZERO_EINVAL for NULL or misaligned pointers. */
+zero_status zero_adamw8_unload(const zero_plan* plan, const uint8_t* d_m8, const uint8_t* d_r8,
+                               const uint8_t* d_scales, void* d_m16, void* d_r16, void* stream);
+
+/* Reduce bucket b and take the AdamW step on its columns in one pass, as zero_reduce_adam_bucket
+ * does for Adam: bit-identical to zero_reduce_shard and the step on the same rows.  Needs
+ * zero_adamw_prepare earlier on the same stream in this step, with the same d_live, d_flag and
+ * d_work.  (A norm to clip by has to be known before: hp.grad_sumsq of zero_adamw_prepare.)
+ * Arguments and errors as zero_reduce_adam_bucket and the steps above. */
+zero_status zero_reduce_adamw_bucket(const zero_plan* plan, int64_t b, const void* d_rows, int64_t row_stride,
+                                     const uint8_t* d_live, float* d_p32, float* d_m, float* d_v,
+                                     const int32_t* d_flag, void* d_arena, void* d_work, void* stream);
+zero_status zero_reduce_adamw8_bucket(const zero_plan* plan, int64_t b, const void* d_rows, int64_t row_stride,
+                                      const uint8_t* d_live, float* d_p32, uint8_t* d_m8, uint8_t* d_r8,
+                                      uint8_t* d_scales, const int32_t* d_flag, void* d_arena, void* d_work,
+                                      void* stream);
+
 /* Thread-local text of the last error ("" if none). */
 const char* zero_last_error(void);
 

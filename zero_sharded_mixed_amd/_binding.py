@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+from dataclasses import dataclass
 from typing import Optional, Sequence
 
 import numpy as np
@@ -29,7 +30,9 @@ EXPORTS = ("zero_plan_create", "zero_plan_create_grouped", "zero_plan_destroy", 
            "zero_pack_bucket", "zero_reduce_shard", "zero_overflow_check", "zero_adam_step", "zero_unpack",
            "zero_shard_init", "zero_pack_bucket_check", "zero_adam_prepare", "zero_reduce_adam_bucket",
            "zero_loss_scaler_init", "zero_loss_scaler_update", "zero_last_error", "zero_adam_step_noalloc",
-           "zero_z3_layer_step", "zero_z3_step")
+           "zero_z3_layer_step", "zero_z3_step", "zero_adamw_get_sizes", "zero_grad_sumsq", "zero_adamw_prepare",
+           "zero_adamw_step", "zero_adamw8_step", "zero_adamw8_load", "zero_adamw8_unload",
+           "zero_reduce_adamw_bucket", "zero_reduce_adamw8_bucket")
 ADAM_NOALLOC_MAX_PARAMS = 131072  # ZERO_ADAM_NOALLOC_MAX_PARAMS
 Z3_MAX_BUCKETS = 4                # ZERO_Z3_MAX_BUCKETS
 
@@ -76,6 +79,36 @@ class zero_z3_pieces(ctypes.Structure):
 class zero_adam_hparams(ctypes.Structure):
     _fields_ = [(f, ctypes.c_double) for f in ("lr", "beta1", "beta2", "eps", "grad_scale")] + \
                [("loss_scaler", ctypes.c_void_p)]
+
+
+class zero_adamw_sizes(ctypes.Structure):
+    _fields_ = [("work_bytes", ctypes.c_int64), ("n_scales", ctypes.c_int64)]
+
+
+class zero_adamw_hparams(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_double) for f in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale",
+                                              "max_norm")] + \
+               [("seed", ctypes.c_uint64)] + \
+               [(f, ctypes.c_void_p) for f in ("loss_scaler", "grad_sumsq", "lr_factor", "decay", "norm_out")]
+
+
+@dataclass
+class AdamWParams:
+    """Hyperparameters of an AdamW step (zero_adamw_hparams); the tensors live on the plan's device
+    and are read when the kernels run."""
+    lr: float
+    beta1: float = 0.9
+    beta2: float = 0.999
+    eps: float = 1e-8
+    weight_decay: float = 0.0
+    grad_scale: float = 1.0
+    max_norm: float = 0.0                        # > 0: clip by the norm that grad_sumsq gives
+    seed: int = 0                                # of the 8-bit states' rounding, in [0, 2^64)
+    loss_scaler: Optional[torch.Tensor] = None   # zero_loss_scaler
+    grad_sumsq: Optional[torch.Tensor] = None    # float64[1], summed over the ranks
+    lr_factor: Optional[torch.Tensor] = None     # float32[1]
+    decay: Optional[torch.Tensor] = None         # float32[n_params]: multiplies weight_decay
+    norm_out: Optional[torch.Tensor] = None      # float32[2]: receives the norm and the coefficient
 
 
 _lib = None
@@ -146,6 +179,15 @@ def _load(path: str) -> ctypes.CDLL:
         "zero_reduce_adam_bucket": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]),
         "zero_loss_scaler_init": (i32, [ctypes.POINTER(zero_loss_scaler), vp, vp]),
         "zero_loss_scaler_update": (i32, [vp, vp, vp]),
+        "zero_adamw_get_sizes": (i32, [vp, ctypes.POINTER(zero_adamw_sizes)]),
+        "zero_grad_sumsq": (i32, [vp] * 7),
+        "zero_adamw_prepare": (i32, [vp, vp, vp, ctypes.POINTER(zero_adamw_hparams), vp, vp, vp]),
+        "zero_adamw_step": (i32, [vp] * 7 + [ctypes.POINTER(zero_adamw_hparams), vp, vp, vp, vp]),
+        "zero_adamw8_step": (i32, [vp] * 8 + [ctypes.POINTER(zero_adamw_hparams), vp, vp, vp, vp]),
+        "zero_adamw8_load": (i32, [vp] * 7),
+        "zero_adamw8_unload": (i32, [vp] * 7),
+        "zero_reduce_adamw_bucket": (i32, [vp, i64, vp, i64] + [vp] * 8),
+        "zero_reduce_adamw8_bucket": (i32, [vp, i64, vp, i64] + [vp] * 9),
         "zero_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sigs.items():
@@ -266,6 +308,9 @@ class Plan:
             _check(lib().zero_plan_param_info(self._h, i, ctypes.byref(info)))
             numels[i] = info.numel
         self.numels = numels
+        sizes = zero_adamw_sizes()
+        _check(lib().zero_adamw_get_sizes(self._h, ctypes.byref(sizes)))
+        self.adamw_work_bytes, self.adamw_n_scales = int(sizes.work_bytes), int(sizes.n_scales)
         bk = zero_bucket_info()
         self.row_stride, self.block_offset = [], []
         for b in range(self.n_buckets):
@@ -513,7 +558,131 @@ def zero_reduce_adam_bucket(plan: Plan, b: int, rows: torch.Tensor, row_stride: 
                                          _stream(stream)))
 
 
+# ------------------------------------------------------------------------------ AdamW --
 
+F64 = (torch.float64,)
+BF16_T = (torch.bfloat16,)
+
+
+def zero_adamw_get_sizes(plan: Plan) -> zero_adamw_sizes:
+    s = zero_adamw_sizes()
+    _check(lib().zero_adamw_get_sizes(plan.handle, ctypes.byref(s)))
+    return s
+
+
+def _adamw_hp(plan: Plan, hp: AdamWParams, what: str) -> zero_adamw_hparams:
+    if not 0 <= int(hp.seed) < 1 << 64:
+        raise ValueError(f"{what}: seed outside [0, 2^64)")
+    return zero_adamw_hparams(hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay, hp.grad_scale, hp.max_norm,
+                              int(hp.seed), _scaler(plan, hp.loss_scaler, what),
+                              _buf(plan, hp.grad_sumsq, what + ": grad_sumsq", 1, F64),
+                              _buf(plan, hp.lr_factor, what + ": lr_factor", 1, F32),
+                              _buf(plan, hp.decay, what + ": decay", plan.n, F32),
+                              _buf(plan, hp.norm_out, what + ": norm_out", 2, F32))
+
+
+def _work(plan: Plan, work: Optional[torch.Tensor], what: str) -> Optional[int]:
+    return _buf(plan, work, what + ": work", plan.adamw_work_bytes, U8)
+
+
+def _states8(plan: Plan, m8, r8, scales, what: str) -> tuple:
+    return (_buf(plan, m8, what + ": m8", plan.shard_numel, elem_size=1),
+            _buf(plan, r8, what + ": r8", plan.shard_numel, elem_size=1),
+            _buf(plan, scales, what + ": scales", 2 * plan.adamw_n_scales, elem_size=1))
+
+
+def zero_grad_sumsq(plan: Plan, g32: torch.Tensor, live: torch.Tensor, sumsq: torch.Tensor, work: torch.Tensor,
+                    flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """sumsq: float64[1], this rank's sum (add the ranks' before a step uses it)."""
+    w = "zero_grad_sumsq"
+    _check(lib().zero_grad_sumsq(plan.handle, _buf(plan, g32, w + ": g32", plan.shard_numel, F32),
+                                 _buf(plan, live, w + ": live", plan.n, U8), _buf(plan, sumsq, w + ": sumsq", 1, F64),
+                                 _buf(plan, flag, w + ": flag", 1, I32), _work(plan, work, w), _stream(stream)))
+
+
+def zero_adamw_prepare(plan: Plan, live: torch.Tensor, steps: torch.Tensor, hp: AdamWParams,
+                       flag: Optional[torch.Tensor], work: torch.Tensor, stream=None) -> None:
+    w = "zero_adamw_prepare"
+    _check(lib().zero_adamw_prepare(plan.handle, _buf(plan, live, w + ": live", plan.n, U8),
+                                    _buf(plan, steps, w + ": steps", plan.n, I32),
+                                    ctypes.byref(_adamw_hp(plan, hp, w)), _buf(plan, flag, w + ": flag", 1, I32),
+                                    _work(plan, work, w), _stream(stream)))
+
+
+def zero_adamw_step(plan: Plan, g32: torch.Tensor, p32: torch.Tensor, m: torch.Tensor, v: torch.Tensor,
+                    live: torch.Tensor, steps: torch.Tensor, hp: AdamWParams, flag: Optional[torch.Tensor],
+                    arena: torch.Tensor, work: torch.Tensor, stream=None) -> None:
+    S, w = plan.shard_numel, "zero_adamw_step"
+    _check(lib().zero_adamw_step(plan.handle, _buf(plan, g32, w + ": g32", S, F32), _buf(plan, p32, w + ": p32", S, F32),
+                                 _buf(plan, m, w + ": m", S, F32), _buf(plan, v, w + ": v", S, F32),
+                                 _buf(plan, live, w + ": live", plan.n, U8),
+                                 _buf(plan, steps, w + ": steps", plan.n, I32), ctypes.byref(_adamw_hp(plan, hp, w)),
+                                 _buf(plan, flag, w + ": flag", 1, I32),
+                                 _buf(plan, arena, w + ": arena", plan.arena_numel, elem_size=2),
+                                 _work(plan, work, w), _stream(stream)))
+
+
+def zero_adamw8_step(plan: Plan, g32: torch.Tensor, p32: torch.Tensor, m8: torch.Tensor, r8: torch.Tensor,
+                     scales: torch.Tensor, live: torch.Tensor, steps: torch.Tensor, hp: AdamWParams,
+                     flag: Optional[torch.Tensor], arena: torch.Tensor, work: torch.Tensor, stream=None) -> None:
+    """m8, r8: one byte per shard column (uint8, or float8_e4m3fn for m8); scales: uint8, twice
+    zero_adamw_get_sizes(plan).n_scales."""
+    S, w = plan.shard_numel, "zero_adamw8_step"
+    _check(lib().zero_adamw8_step(plan.handle, _buf(plan, g32, w + ": g32", S, F32),
+                                  _buf(plan, p32, w + ": p32", S, F32), *_states8(plan, m8, r8, scales, w),
+                                  _buf(plan, live, w + ": live", plan.n, U8),
+                                  _buf(plan, steps, w + ": steps", plan.n, I32), ctypes.byref(_adamw_hp(plan, hp, w)),
+                                  _buf(plan, flag, w + ": flag", 1, I32),
+                                  _buf(plan, arena, w + ": arena", plan.arena_numel, elem_size=2),
+                                  _work(plan, work, w), _stream(stream)))
+
+
+def zero_adamw8_load(plan: Plan, m: torch.Tensor, v: torch.Tensor, m8: torch.Tensor, r8: torch.Tensor,
+                     scales: torch.Tensor, stream=None) -> None:
+    """8-bit states (m8, r8, scales) from 32-bit ones."""
+    S, w = plan.shard_numel, "zero_adamw8_load"
+    _check(lib().zero_adamw8_load(plan.handle, _buf(plan, m, w + ": m", S, F32), _buf(plan, v, w + ": v", S, F32),
+                                  *_states8(plan, m8, r8, scales, w), _stream(stream)))
+
+
+def zero_adamw8_unload(plan: Plan, m8: torch.Tensor, r8: torch.Tensor, scales: torch.Tensor, m16: torch.Tensor,
+                       r16: torch.Tensor, stream=None) -> None:
+    """m16, r16: bfloat16, receive the momentum and the root of the variance that the codes stand for."""
+    S, w = plan.shard_numel, "zero_adamw8_unload"
+    _check(lib().zero_adamw8_unload(plan.handle, *_states8(plan, m8, r8, scales, w),
+                                    _buf(plan, m16, w + ": m16", S, BF16_T), _buf(plan, r16, w + ": r16", S, BF16_T),
+                                    _stream(stream)))
+
+
+def zero_reduce_adamw_bucket(plan: Plan, b: int, rows: torch.Tensor, row_stride: int, live: torch.Tensor,
+                             p32: torch.Tensor, m: torch.Tensor, v: torch.Tensor, flag: Optional[torch.Tensor],
+                             arena: torch.Tensor, work: torch.Tensor, stream=None) -> None:
+    """rows as in zero_reduce_shard; needs zero_adamw_prepare earlier in the step, same stream and work."""
+    S, w = plan.shard_numel, "zero_reduce_adamw_bucket"
+    _check(lib().zero_reduce_adamw_bucket(plan.handle, b, _buf(plan, rows, w + ": rows", plan.rows_elems(b, row_stride),
+                                                               elem_size=2),
+                                          row_stride, _buf(plan, live, w + ": live", plan.n, U8),
+                                          _buf(plan, p32, w + ": p32", S, F32), _buf(plan, m, w + ": m", S, F32),
+                                          _buf(plan, v, w + ": v", S, F32), _buf(plan, flag, w + ": flag", 1, I32),
+                                          _buf(plan, arena, w + ": arena", plan.arena_numel, elem_size=2),
+                                          _work(plan, work, w), _stream(stream)))
+
+
+def zero_reduce_adamw8_bucket(plan: Plan, b: int, rows: torch.Tensor, row_stride: int, live: torch.Tensor,
+                              p32: torch.Tensor, m8: torch.Tensor, r8: torch.Tensor, scales: torch.Tensor,
+                              flag: Optional[torch.Tensor], arena: torch.Tensor, work: torch.Tensor,
+                              stream=None) -> None:
+    S, w = plan.shard_numel, "zero_reduce_adamw8_bucket"
+    _check(lib().zero_reduce_adamw8_bucket(plan.handle, b, _buf(plan, rows, w + ": rows",
+                                                                plan.rows_elems(b, row_stride), elem_size=2),
+                                           row_stride, _buf(plan, live, w + ": live", plan.n, U8),
+                                           _buf(plan, p32, w + ": p32", S, F32), *_states8(plan, m8, r8, scales, w),
+                                           _buf(plan, flag, w + ": flag", 1, I32),
+                                           _buf(plan, arena, w + ": arena", plan.arena_numel, elem_size=2),
+                                           _work(plan, work, w), _stream(stream)))
+
+
+# ---------------------------------------------------------------------- loss scaler --
 
 def zero_loss_scaler_init(cfg: zero_loss_scaler, scaler: torch.Tensor, stream=None) -> None:
     """scaler: device tensor of at least LOSS_SCALER_BYTES bytes (e.g. int32[8])."""

@@ -1,0 +1,225 @@
+// adamw.hip — the AdamW step over rank r's shard with its states in 32 bits, with the 16-bit
+// write of the updated parameters into row r of every bucket's all-gather block, and the prepare
+// launch that the 32-bit, the 8-bit and the fused steps share.
+//
+// Two launches, as for zero_adam_step.  adamw_prepare_kernel (one thread per parameter) reads the
+// overflow flag, advances the live parameters' step counts and forms every scalar of the step in
+// double: the clip coefficient from the sum of squares, the gradient multiplier, the rate from
+// the schedule's factor, and per parameter the step size, the bias correction and the decay.
+// adamw_kernel then streams the shard: 16 bytes in and 14 out per element, bound by memory.
+#include <cmath>
+
+#include "zs_adamw.h"
+
+namespace zs {
+
+struct AdamWHost {  // the hyperparameters by value, and the rounding noise's key without the step count
+    double lr, beta1, beta2, eps, weight_decay, grad_scale, max_norm;
+    const zero_loss_scaler* scaler;
+    const double* sumsq;
+    const float* lr_factor;
+    const float* decay;
+    float* norm_out;
+    uint32_t key;
+};
+
+__global__ void adamw_prepare_kernel(DevPlan P, const uint8_t* __restrict__ live, int32_t* __restrict__ steps,
+                                     const int32_t* __restrict__ flag, AdamWHost H, float4* __restrict__ scal,
+                                     float* __restrict__ consts) {
+    if (flag && *flag) return;
+    const int64_t gid = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
+    if (gid == 0) {
+        double mult = H.scaler ? H.grad_scale / double(H.scaler->scale) : H.grad_scale;
+        if (H.sumsq) {
+            // a sum that is not finite gives a multiplier that is not: without a flag that skips
+            // the step, the parameters show it
+            const double norm = sqrt(*H.sumsq) * fabs(mult);
+            double coef = H.max_norm > 0.0 ? H.max_norm / (norm + 1e-6) : 1.0;
+            coef = coef > 1.0 ? 1.0 : coef;
+            if (!(norm < __builtin_inf())) coef = __builtin_nan("");
+            if (H.norm_out) {
+                H.norm_out[0] = float(norm);
+                H.norm_out[1] = float(coef);
+            }
+            mult = mult * coef;
+        }
+        consts[AC_BETA1] = float(H.beta1);
+        consts[AC_BETA2] = float(H.beta2);
+        consts[AC_C1] = float(1.0 - H.beta1);
+        consts[AC_C2] = float(1.0 - H.beta2);
+        consts[AC_EPS] = float(H.eps);
+        consts[AC_GSCALE] = float(mult);
+    }
+    const double lr = H.lr_factor ? H.lr * double(*H.lr_factor) : H.lr;
+    for (int64_t i = gid; i < P.n; i += int64_t(gridDim.x) * blockDim.x) {
+        if (!live[i]) continue;
+        const int32_t t = steps[i] + 1;
+        steps[i] = t;
+        const double bc1 = 1.0 - pow(H.beta1, double(t));
+        const double bc2 = 1.0 - pow(H.beta2, double(t));
+        const double shrink = lr * H.weight_decay * (H.decay ? double(H.decay[i]) : 1.0);
+        scal[i] = make_float4(float(lr / bc1), float(1.0 / sqrt(bc2)), float(shrink),
+                              __uint_as_float(mix32(uint32_t(t) ^ H.key)));
+    }
+}
+
+struct AdamWArgs {
+    const float* g32;
+    float* p32;
+    float* m;
+    float* v;
+    const uint8_t* live;
+    const float4* scal;
+    const float* consts;
+    const int32_t* flag;
+    uint16_t* arena;
+};
+
+// One block per tile of 2048 columns, as in adam_kernel: a tile inside one live parameter goes
+// lane-strided with nontemporal loads, the others 8 columns in a row per thread, element by
+// element where parameters, dead slots or a row gap meet.
+template <int DT>
+__global__ __launch_bounds__(kBlock) void adamw_kernel(DevPlan P, AdamWArgs A) {
+    if (A.flag && *A.flag) return;
+    const AdamK K = load_adam_consts(A.consts);
+    for (int64_t j = blockIdx.x; j < P.n_tiles; j += gridDim.x) {
+        const int64_t x0 = j << kTileShift;
+        const int64_t iu = ld_const(P.tile_first, j);
+        const int64_t ic = iu < P.n ? iu : P.n - 1;
+        if (iu < P.n && ld_const(P.off, ic) <= x0 && ld_const(P.end, ic) >= x0 + kTileCols) {
+            if (!ld_const(A.live, ic)) continue;
+            const AdamWScal s = ld_const_scal(A.scal, ic);
+            const int32_t b = ld_const(P.bucket, ic);
+            const int64_t O = ld_const(P.b_base, b);
+            uint16_t* lp = A.arena + P.nd * O + P.rank * ld_const(P.b_stride, b) + (x0 - O);
+            float4 g[2], p[2], m[2], v[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t x = x0 + quad_col(q);
+                g[q] = load4f_nt(A.g32 + x);
+                p[q] = load4f_nt(A.p32 + x);
+                m[q] = load4f_nt(A.m + x);
+                v[q] = load4f_nt(A.v + x);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t x = x0 + quad_col(q);
+                adamw_quad<DT>(K, s, g[q], p[q], m[q], v[q], A.p32 + x, A.m + x, A.v + x, lp + quad_col(q));
+            }
+            continue;
+        }
+        const int64_t x = x0 + int64_t(threadIdx.x) * kChunk;
+        if (x >= P.shard_numel) continue;
+        int64_t i = param_of_column(P, x);
+        if (i < P.n && P.off[i] <= x && x + kChunk <= P.end[i]) {
+            if (!A.live[i]) continue;
+            const AdamWScal s = scal_of(A.scal[i]);
+            const int32_t b = P.bucket[i];
+            const int64_t O = P.b_base[b];
+            uint16_t* lp = A.arena + P.nd * O + P.rank * P.b_stride[b] + (x - O);
+            float4 g[2], p[2], m[2], v[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                g[q] = load4f(A.g32 + x + 4 * q);
+                p[q] = load4f(A.p32 + x + 4 * q);
+                m[q] = load4f(A.m + x + 4 * q);
+                v[q] = load4f(A.v + x + 4 * q);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                adamw_quad<DT>(K, s, g[q], p[q], m[q], v[q], A.p32 + x + 4 * q, A.m + x + 4 * q, A.v + x + 4 * q,
+                               lp + 4 * q);
+            continue;
+        }
+#pragma unroll
+        for (int t = 0; t < kChunk; ++t) {
+            const int64_t xt = x + t;
+            while (i < P.n && P.end[i] <= xt) ++i;
+            if (!(i < P.n && P.off[i] <= xt) || !A.live[i]) continue;
+            const int32_t b = P.bucket[i];
+            const int64_t O = P.b_base[b];
+            float p = gptr(A.p32)[xt], m = gptr(A.m)[xt], v = gptr(A.v)[xt];
+            adamw_elem(K, scal_of(A.scal[i]), gptr(A.g32)[xt], p, m, v);
+            gptr(A.p32)[xt] = p;
+            gptr(A.m)[xt] = m;
+            gptr(A.v)[xt] = v;
+            gptr(A.arena)[P.nd * O + P.rank * P.b_stride[b] + (xt - O)] = from_f32<DT>(p);
+        }
+    }
+}
+
+zero_status check_work(const void* work, const char* who) {
+    if (!work || !host_aligned16(work)) return fail(ZERO_EINVAL, "%s: work must be a 16-byte aligned pointer", who);
+    return ZERO_OK;
+}
+
+zero_status launch_adamw_prepare(const zero_plan* plan, const uint8_t* d_live, int32_t* d_steps,
+                                 const zero_adamw_hparams* hp, const int32_t* d_flag, void* work, hipStream_t s,
+                                 const char* who) {
+    if (!d_live || !d_steps || !hp) return fail(ZERO_EINVAL, "%s: NULL pointer", who);
+    const zero_status st = check_work(work, who);
+    if (st != ZERO_OK) return st;
+    const auto at_least_0 = [](double x) { return std::isfinite(x) && x >= 0.0; };
+    if (!at_least_0(hp->lr) || !(hp->beta1 >= 0.0) || !(hp->beta1 < 1.0) || !(hp->beta2 >= 0.0) || !(hp->beta2 < 1.0) ||
+        !at_least_0(hp->weight_decay) || !std::isfinite(hp->grad_scale) || !at_least_0(hp->max_norm))
+        return fail(ZERO_EINVAL, "%s: hyperparameters out of range", who);
+    // eps keeps the padding's update, 0 / (0 + eps), a number
+    if (!std::isfinite(hp->eps) || !(float(hp->eps) > 0.0f))
+        return fail(ZERO_EINVAL, "%s: eps must be positive in fp32", who);
+    if (!hp->grad_sumsq && (hp->max_norm > 0.0 || hp->norm_out))
+        return fail(ZERO_EINVAL, "%s: max_norm and norm_out need grad_sumsq", who);
+    if (reinterpret_cast<uintptr_t>(hp->grad_sumsq) % 8 != 0 ||
+        (reinterpret_cast<uintptr_t>(hp->loss_scaler) | reinterpret_cast<uintptr_t>(hp->lr_factor) |
+         reinterpret_cast<uintptr_t>(hp->decay) | reinterpret_cast<uintptr_t>(hp->norm_out)) % 4 != 0)
+        return fail(ZERO_EINVAL, "%s: misaligned hyperparameter pointer", who);
+    uint32_t key = mix32(uint32_t(plan->rank) ^ kRoot3);
+    key = mix32(key ^ uint32_t(hp->seed));
+    key = mix32(key ^ uint32_t(hp->seed >> 32));
+    const AdamWHost H{hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay, hp->grad_scale, hp->max_norm,
+                      hp->loss_scaler, hp->grad_sumsq, hp->lr_factor, hp->decay, hp->norm_out, key};
+    adamw_prepare_kernel<<<grid_for((plan->n + 255) / 256, 1024), 256, 0, s>>>(
+        plan->dev, d_live, d_steps, d_flag, H, work_scal(work), work_consts(work));
+    return check_launch(who);
+}
+
+}  // namespace zs
+
+using namespace zs;
+
+extern "C" zero_status zero_adamw_get_sizes(const zero_plan* plan, zero_adamw_sizes* out) {
+    if (!plan || !out) return fail(ZERO_EINVAL, "zero_adamw_get_sizes: NULL argument");
+    out->work_bytes = work_bytes(plan->n);
+    out->n_scales = ((plan->shard_numel + kRun - 1) >> kRunShift) + plan->n;
+    return ZERO_OK;
+}
+
+extern "C" zero_status zero_adamw_prepare(const zero_plan* plan, const uint8_t* d_live, int32_t* d_steps,
+                                          const zero_adamw_hparams* hp, const int32_t* d_flag, void* d_work,
+                                          void* stream) {
+    const zero_status st = check_device(plan);
+    if (st != ZERO_OK) return st;
+    return launch_adamw_prepare(plan, d_live, d_steps, hp, d_flag, d_work, (hipStream_t)stream, "zero_adamw_prepare");
+}
+
+extern "C" zero_status zero_adamw_step(const zero_plan* plan, const float* d_g32, float* d_p32, float* d_m, float* d_v,
+                                       const uint8_t* d_live, int32_t* d_steps, const zero_adamw_hparams* hp,
+                                       const int32_t* d_flag, void* d_arena, void* d_work, void* stream) {
+    const char* who = "zero_adamw_step";
+    zero_status st = check_device(plan);
+    if (st != ZERO_OK) return st;
+    // an empty shard still advances the step counts of live parameters; its arrays may be NULL
+    if (plan->shard_numel != 0 && (!d_g32 || !d_p32 || !d_m || !d_v || !d_arena))
+        return fail(ZERO_EINVAL, "%s: NULL pointer", who);
+    if (!host_aligned16(d_g32) || !host_aligned16(d_p32) || !host_aligned16(d_m) || !host_aligned16(d_v) ||
+        !host_aligned16(d_arena))
+        return fail(ZERO_EINVAL, "%s: shard arrays and arena must be 16-byte aligned", who);
+    hipStream_t s = (hipStream_t)stream;
+    if ((st = launch_adamw_prepare(plan, d_live, d_steps, hp, d_flag, d_work, s, who)) != ZERO_OK) return st;
+    if (plan->shard_numel == 0) return ZERO_OK;
+    const AdamWArgs A{d_g32, d_p32, d_m, d_v, d_live, work_scal(d_work), work_consts(d_work), d_flag,
+                      static_cast<uint16_t*>(d_arena)};
+    const int g = grid_for(plan->dev.n_tiles);
+    if (plan->dtype == ZERO_BF16) adamw_kernel<ZERO_BF16><<<g, kBlock, kTwoBlocksLds, s>>>(plan->dev, A);
+    else adamw_kernel<ZERO_FP16><<<g, kBlock, kTwoBlocksLds, s>>>(plan->dev, A);
+    return check_launch(who);
+}

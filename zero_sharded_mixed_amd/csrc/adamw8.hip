@@ -1,0 +1,219 @@
+// adamw8.hip — the AdamW step over rank r's shard with its momentum and the root of its variance
+// in 8 bits (the format is in zs_adamw.h), and the conversions from and to wider states.
+//
+// The step reads g32, p32 and two codes and writes p32, two codes and the 16-bit parameter: 10
+// bytes in and 8 out per element (30 with 32-bit states), and the states take 2 bytes instead of 8.
+// A wavefront takes a run of 256 columns, 4 a lane, so that a block's largest magnitude is one
+// reduction inside the wavefront and every array is read and written in whole lines.
+#include <cmath>
+
+#include "zs_adamw.h"
+
+namespace zs {
+
+// First column of the run that pass q of a block's tile gives the wavefront's lane, and its own.
+__device__ __forceinline__ int64_t run_of(int64_t x) { return x & ~(kRun - 1); }
+
+template <int DT>
+__global__ __launch_bounds__(kBlock) void adamw8_kernel(DevPlan P, AdamW8Args A, const float* __restrict__ g32) {
+    if (A.flag && *A.flag) return;
+    __shared__ RunMax scratch[kBlock / 64];
+    const AdamK K = load_adam_consts(A.consts);
+    for (int64_t j = blockIdx.x; j < P.n_tiles; j += gridDim.x) {
+        const int64_t x0 = j << kTileShift;
+        const int64_t iu = ld_const(P.tile_first, j);
+        const int64_t ic = iu < P.n ? iu : P.n - 1;
+        if (iu < P.n && ld_const(P.off, ic) <= x0 && ld_const(P.end, ic) >= x0 + kTileCols) {
+            if (!ld_const(A.live, ic)) continue;
+            const AdamWScal s = ld_const_scal(A.scal, ic);
+            const int32_t b = ld_const(P.bucket, ic);
+            const int64_t O = ld_const(P.b_base, b);
+            uint16_t* lp = A.arena + P.nd * O + P.rank * ld_const(P.b_stride, b) + (x0 - O);
+            float4 g[2];
+            Run8 r[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t x = x0 + quad_col(q);
+                g[q] = load4f_nt(g32 + x);
+                r[q] = run8_load(A, x, (x >> kRunShift) + ic);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t x = x0 + quad_col(q);
+                run8_step<DT>(K, s, A, x, (x >> kRunShift) + ic, g[q], r[q], lp + quad_col(q));
+            }
+            continue;
+        }
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+            const int64_t x = x0 + quad_col(q);
+            const int64_t run = run_of(x);
+            if (run >= P.shard_numel) break;
+            const int64_t i = param_of_column(P, x);
+            // a parameter that covers the run is the one that every lane found
+            if (i < P.n && P.off[i] <= run && P.end[i] >= run + kRun) {
+                if (!A.live[i]) continue;
+                const int32_t b = P.bucket[i];
+                const int64_t O = P.b_base[b], block = (run >> kRunShift) + i;
+                run8_step<DT>(K, scal_of(A.scal[i]), A, x, block, load4f_nt(g32 + x), run8_load(A, x, block),
+                              A.arena + P.nd * O + P.rank * P.b_stride[b] + (x - O));
+                continue;
+            }
+            run8_mixed<DT>(P, K, A, &scratch[threadIdx.x >> 6], x, i, 0, P.shard_numel,
+                           [&](int64_t xt) { return gptr(g32)[xt]; });
+        }
+    }
+}
+
+// Codes to the nearest (ties to even) of 32-bit states, every parameter's, live or not.  A run at
+// a time through the wavefront's scratch.
+__global__ __launch_bounds__(kBlock) void adamw8_load_kernel(DevPlan P, const float* __restrict__ mm,
+                                                             const float* __restrict__ vv, uint8_t* __restrict__ m8,
+                                                             uint8_t* __restrict__ r8, uint16_t* __restrict__ scales) {
+    __shared__ RunMax scratch[kBlock / 64];
+    RunMax* S = &scratch[threadIdx.x >> 6];
+    for (int64_t j = blockIdx.x; j < P.n_tiles; j += gridDim.x) {
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+            const int64_t x = (j << kTileShift) + quad_col(q);
+            const int64_t run = run_of(x);
+            if (run >= P.shard_numel) break;
+            int64_t i = param_of_column(P, x);
+            const uint32_t l4 = uint32_t(x - run);
+            float m[4], r[4];
+            int64_t own[4];
+            uint32_t first[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                S->m[l4 + t] = 0;
+                S->r[l4 + t] = 0;
+            }
+            wave_lds_fence();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int64_t xt = x + t;
+                own[t] = -1;
+                while (i < P.n && P.end[i] <= xt) ++i;
+                if (!(i < P.n && P.off[i] <= xt)) continue;
+                own[t] = i;
+                first[t] = uint32_t((P.off[i] > run ? P.off[i] : run) - run);
+                m[t] = gptr(mm)[xt];
+                r[t] = sqrtf(gptr(vv)[xt]);
+                atomicMax(&S->m[first[t]], abs_bits(m[t]));
+                atomicMax(&S->r[first[t]], abs_bits(r[t]));
+            }
+            wave_lds_fence();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (own[t] < 0) continue;
+                const int64_t xt = x + t;
+                const uint32_t mb = moment_byte(S->m[first[t]]), rb = root_byte(S->r[first[t]]);
+                gptr(m8)[xt] = mb == kScaleNan ? 0 : uint8_t(moment_code_near(m[t], inverse_of_byte(mb)));
+                gptr(r8)[xt] = rb == kScaleNan ? 0 : uint8_t(root_code_near(r[t], inverse_of_byte(rb)));
+                if (l4 + t == first[t]) gptr(scales)[(run >> kRunShift) + own[t]] = uint16_t(mb | (rb << 8));
+            }
+            wave_lds_fence();
+        }
+    }
+}
+
+// The states' values in bf16, which holds them exactly: 2 bytes in and 4 out per element.
+__device__ __forceinline__ uint32_t bf16_bits(float f) { return __float_as_uint(f) >> 16; }
+__device__ __forceinline__ uint64_t bf16x4(const float (&f)[4]) {
+    return uint64_t(bf16_bits(f[0]) | (bf16_bits(f[1]) << 16)) | uint64_t(bf16_bits(f[2]) | (bf16_bits(f[3]) << 16)) << 32;
+}
+__global__ __launch_bounds__(kBlock) void adamw8_unload_kernel(DevPlan P, const uint8_t* __restrict__ m8,
+                                                               const uint8_t* __restrict__ r8,
+                                                               const uint16_t* __restrict__ scales,
+                                                               uint16_t* __restrict__ m16, uint16_t* __restrict__ r16) {
+    for (int64_t j = blockIdx.x; j < P.n_tiles; j += gridDim.x) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int64_t x = (j << kTileShift) + quad_col(q);
+            if (x >= P.shard_numel) break;
+            int64_t i = param_of_column(P, x);
+            if (i < P.n && P.off[i] <= x && x + 4 <= P.end[i]) {
+                const uint32_t pair = gptr(scales)[(x >> kRunShift) + i];
+                const float ms = pow2_of_byte(pair & 0xffu), rs = pow2_of_byte(pair >> 8);
+                const uint32_t mw = *gptr(reinterpret_cast<const uint32_t*>(m8 + x));
+                const uint32_t rw = *gptr(reinterpret_cast<const uint32_t*>(r8 + x));
+                float m[4], r[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    m[t] = moment_value((mw >> (8 * t)) & 0xffu) * ms;
+                    r[t] = root_value((rw >> (8 * t)) & 0xffu) * rs;
+                }
+                store8(m16 + x, bf16x4(m));
+                store8(r16 + x, bf16x4(r));
+                continue;
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int64_t xt = x + t;
+                while (i < P.n && P.end[i] <= xt) ++i;
+                if (!(i < P.n && P.off[i] <= xt)) continue;
+                const uint32_t pair = gptr(scales)[(x >> kRunShift) + i];
+                gptr(m16)[xt] = uint16_t(bf16_bits(moment_value(gptr(m8)[xt]) * pow2_of_byte(pair & 0xffu)));
+                gptr(r16)[xt] = uint16_t(bf16_bits(root_value(gptr(r8)[xt]) * pow2_of_byte(pair >> 8)));
+            }
+        }
+    }
+}
+
+}  // namespace zs
+
+using namespace zs;
+
+extern "C" zero_status zero_adamw8_step(const zero_plan* plan, const float* d_g32, float* d_p32, uint8_t* d_m8,
+                                        uint8_t* d_r8, uint8_t* d_scales, const uint8_t* d_live, int32_t* d_steps,
+                                        const zero_adamw_hparams* hp, const int32_t* d_flag, void* d_arena,
+                                        void* d_work, void* stream) {
+    const char* who = "zero_adamw8_step";
+    zero_status st = check_device(plan);
+    if (st != ZERO_OK) return st;
+    if (plan->shard_numel != 0 && (!d_g32 || !d_p32 || !d_m8 || !d_r8 || !d_scales || !d_arena))
+        return fail(ZERO_EINVAL, "%s: NULL pointer", who);
+    if (!host_aligned16(d_g32) || !host_aligned16(d_p32) || !host_aligned16(d_m8) || !host_aligned16(d_r8) ||
+        !host_aligned16(d_scales) || !host_aligned16(d_arena))
+        return fail(ZERO_EINVAL, "%s: shard arrays, scales and arena must be 16-byte aligned", who);
+    hipStream_t s = (hipStream_t)stream;
+    if ((st = launch_adamw_prepare(plan, d_live, d_steps, hp, d_flag, d_work, s, who)) != ZERO_OK) return st;
+    if (plan->shard_numel == 0) return ZERO_OK;
+    const AdamW8Args A{d_p32, d_m8, d_r8, reinterpret_cast<uint16_t*>(d_scales), d_live, work_scal(d_work),
+                       work_consts(d_work), d_flag, static_cast<uint16_t*>(d_arena)};
+    const int g = grid_for(plan->dev.n_tiles);
+    if (plan->dtype == ZERO_BF16) adamw8_kernel<ZERO_BF16><<<g, kBlock, 0, s>>>(plan->dev, A, d_g32);
+    else adamw8_kernel<ZERO_FP16><<<g, kBlock, 0, s>>>(plan->dev, A, d_g32);
+    return check_launch(who);
+}
+
+extern "C" zero_status zero_adamw8_load(const zero_plan* plan, const float* d_m, const float* d_v, uint8_t* d_m8,
+                                        uint8_t* d_r8, uint8_t* d_scales, void* stream) {
+    const char* who = "zero_adamw8_load";
+    const zero_status st = check_device(plan);
+    if (st != ZERO_OK) return st;
+    if (plan->shard_numel == 0) return ZERO_OK;
+    if (!d_m || !d_v || !d_m8 || !d_r8 || !d_scales) return fail(ZERO_EINVAL, "%s: NULL pointer", who);
+    if (!host_aligned16(d_m) || !host_aligned16(d_v) || !host_aligned16(d_m8) || !host_aligned16(d_r8) ||
+        !host_aligned16(d_scales))
+        return fail(ZERO_EINVAL, "%s: state arrays and scales must be 16-byte aligned", who);
+    adamw8_load_kernel<<<grid_for(plan->dev.n_tiles), kBlock, 0, (hipStream_t)stream>>>(
+        plan->dev, d_m, d_v, d_m8, d_r8, reinterpret_cast<uint16_t*>(d_scales));
+    return check_launch(who);
+}
+
+extern "C" zero_status zero_adamw8_unload(const zero_plan* plan, const uint8_t* d_m8, const uint8_t* d_r8,
+                                          const uint8_t* d_scales, void* d_m16, void* d_r16, void* stream) {
+    const char* who = "zero_adamw8_unload";
+    const zero_status st = check_device(plan);
+    if (st != ZERO_OK) return st;
+    if (plan->shard_numel == 0) return ZERO_OK;
+    if (!d_m8 || !d_r8 || !d_scales || !d_m16 || !d_r16) return fail(ZERO_EINVAL, "%s: NULL pointer", who);
+    if (!host_aligned16(d_m8) || !host_aligned16(d_r8) || !host_aligned16(d_scales) || !host_aligned16(d_m16) ||
+        !host_aligned16(d_r16))
+        return fail(ZERO_EINVAL, "%s: state arrays and scales must be 16-byte aligned", who);
+    adamw8_unload_kernel<<<grid_for(plan->dev.n_tiles), kBlock, 0, (hipStream_t)stream>>>(
+        plan->dev, d_m8, d_r8, reinterpret_cast<const uint16_t*>(d_scales), static_cast<uint16_t*>(d_m16),
+        static_cast<uint16_t*>(d_r16));
+    return check_launch(who);
+}

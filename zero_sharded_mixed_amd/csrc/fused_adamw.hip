@@ -1,0 +1,229 @@
+// fused_adamw.hip — the reduce and the AdamW step of one bucket in a single pass, with 32-bit or
+// 8-bit states: the fused path of fused.hip (same rows, same order of sums, same overflow verdict
+// from the inputs) with the steps of adamw.hip and adamw8.hip.  The reduced gradient never goes
+// to memory, so an element moves 2 Nd bytes of rows and 26 bytes of states and parameters (14 with
+// 8-bit states), and the results are bit-identical to zero_reduce_shard and the step of its own.
+#include "zs_adamw.h"
+
+namespace zs {
+
+// A tile inside one live parameter: every thread sums 8 columns in a row (16-byte loads of every
+// rank's row), the sums go through LDS, and the step takes the tile lane-strided.  The tile's
+// reduced gradient as the thread's two quads:
+template <int DT>
+__device__ __forceinline__ void tile_sums(float4* g_lds, const uint16_t* rows_u, int64_t nd, int64_t row_stride) {
+    float acc[8];
+    reduce_rows8<DT, kRowsLow, true>(rows_u, threadIdx.x * kChunk, nd, row_stride, acc);
+    g_lds[2 * threadIdx.x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    g_lds[2 * threadIdx.x + 1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+}
+
+struct BucketRows {
+    int64_t base, row, stride, tile0, n_tile;
+    const uint16_t* rows;
+    int64_t row_stride;
+};
+
+template <int DT>
+__global__ __launch_bounds__(kBlock) void reduce_adamw_kernel(DevPlan P, BucketRows B, const uint8_t* __restrict__ live,
+                                                              float* __restrict__ p32, float* __restrict__ m,
+                                                              float* __restrict__ v, const float4* __restrict__ scal,
+                                                              const float* __restrict__ consts,
+                                                              const int32_t* __restrict__ flag,
+                                                              uint16_t* __restrict__ arena) {
+    if (flag && *flag) return;
+    __shared__ float4 g_lds[kTileCols / 4];
+    const AdamK K = load_adam_consts(consts);
+    uint16_t* const lp_row = arena + P.nd * B.base + P.rank * B.stride;  // row r of the bucket's block
+    for (int64_t w = blockIdx.x; w < B.n_tile; w += gridDim.x) {
+        const int64_t j = B.tile0 + w;
+        const int64_t x0 = j << kTileShift;
+        const int64_t iu = ld_const(P.tile_first, j);
+        const int64_t ic = iu < P.n ? iu : P.n - 1;
+        if (iu < P.n && ld_const(P.off, ic) <= x0 && ld_const(P.end, ic) >= x0 + kTileCols) {
+            if (!ld_const(live, ic)) continue;
+            const AdamWScal s = ld_const_scal(scal, ic);
+            tile_sums<DT>(g_lds, B.rows + (x0 - B.base), P.nd, B.row_stride);
+            float4 p4[2], m4[2], v4[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t x = x0 + quad_col(q);
+                p4[q] = load4f_nt(p32 + x);
+                m4[q] = load4f_nt(m + x);
+                v4[q] = load4f_nt(v + x);
+            }
+            __syncthreads();
+            float4 g4[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) g4[q] = g_lds[quad_col(q) / 4];
+            __syncthreads();  // the LDS is free for the block's next tile
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t x = x0 + quad_col(q);
+                adamw_quad<DT>(K, s, g4[q], p4[q], m4[q], v4[q], p32 + x, m + x, v + x, lp_row + (x - B.base));
+            }
+            continue;
+        }
+        const int64_t x = x0 + int64_t(threadIdx.x) * kChunk;
+        const int64_t c = x - B.base;
+        if (c < 0 || c >= B.row) continue;  // outside the bucket, or entirely in the row gap
+        int64_t i = param_of_column(P, x);
+        const unsigned mask = live_mask8(P, live, x, i);
+        if (mask == 0) continue;
+        float acc[8];
+        reduce_rows8<DT, kRowsPipe, true>(B.rows + (x0 - B.base), threadIdx.x * kChunk, P.nd, B.row_stride, acc);
+        if (mask == 0xffu && i < P.n && P.off[i] <= x && x + kChunk <= P.end[i]) {
+            const AdamWScal s = scal_of(scal[i]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t xq = x + 4 * q;
+                adamw_quad<DT>(K, s, make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]),
+                               load4f(p32 + xq), load4f(m + xq), load4f(v + xq), p32 + xq, m + xq, v + xq,
+                               lp_row + c + 4 * q);
+            }
+            continue;
+        }
+#pragma unroll
+        for (int t = 0; t < kChunk; ++t) {
+            if (!(mask & (1u << t))) continue;
+            const int64_t xt = x + t;
+            while (i < P.n && P.end[i] <= xt) ++i;
+            float pe = gptr(p32)[xt], me = gptr(m)[xt], ve = gptr(v)[xt];
+            adamw_elem(K, scal_of(scal[i]), acc[t], pe, me, ve);
+            gptr(p32)[xt] = pe;
+            gptr(m)[xt] = me;
+            gptr(v)[xt] = ve;
+            gptr(lp_row)[c + t] = from_f32<DT>(pe);
+        }
+    }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kBlock) void reduce_adamw8_kernel(DevPlan P, BucketRows B, AdamW8Args A) {
+    if (A.flag && *A.flag) return;
+    __shared__ float4 g_lds[kTileCols / 4];
+    __shared__ RunMax scratch[kBlock / 64];
+    const AdamK K = load_adam_consts(A.consts);
+    uint16_t* const lp_row = A.arena + P.nd * B.base + P.rank * B.stride;
+    for (int64_t w = blockIdx.x; w < B.n_tile; w += gridDim.x) {
+        const int64_t j = B.tile0 + w;
+        const int64_t x0 = j << kTileShift;
+        const int64_t iu = ld_const(P.tile_first, j);
+        const int64_t ic = iu < P.n ? iu : P.n - 1;
+        if (iu < P.n && ld_const(P.off, ic) <= x0 && ld_const(P.end, ic) >= x0 + kTileCols) {
+            if (!ld_const(A.live, ic)) continue;
+            const AdamWScal s = ld_const_scal(A.scal, ic);
+            tile_sums<DT>(g_lds, B.rows + (x0 - B.base), P.nd, B.row_stride);
+            Run8 r[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t x = x0 + quad_col(q);
+                r[q] = run8_load(A, x, (x >> kRunShift) + ic);
+            }
+            __syncthreads();
+            float4 g4[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) g4[q] = g_lds[quad_col(q) / 4];
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t x = x0 + quad_col(q);
+                run8_step<DT>(K, s, A, x, (x >> kRunShift) + ic, g4[q], r[q], lp_row + (x - B.base));
+            }
+            continue;
+        }
+        // The other tiles: the bucket's live columns are summed into the LDS as above (the rest of
+        // it is not read), then every wavefront takes its two runs.
+        {
+            const int64_t x = x0 + int64_t(threadIdx.x) * kChunk;
+            const int64_t c = x - B.base;
+            if (c >= 0 && c < B.row && live_mask8(P, A.live, x, param_of_column(P, x)) != 0) {
+                float acc[8];
+                reduce_rows8<DT, kRowsPipe, true>(B.rows + (x0 - B.base), threadIdx.x * kChunk, P.nd, B.row_stride, acc);
+                g_lds[2 * threadIdx.x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                g_lds[2 * threadIdx.x + 1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+            }
+        }
+        __syncthreads();
+        const float* g = reinterpret_cast<const float*>(g_lds);
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+            const int64_t x = x0 + quad_col(q);
+            const int64_t run = x & ~(kRun - 1);
+            if (run >= B.base + B.row || run + kRun <= B.base) continue;
+            const int64_t i = param_of_column(P, x);
+            if (i < P.n && P.off[i] <= run && P.end[i] >= run + kRun) {
+                if (!A.live[i]) continue;
+                const int64_t block = (run >> kRunShift) + i;
+                run8_step<DT>(K, scal_of(A.scal[i]), A, x, block, g_lds[quad_col(q) / 4], run8_load(A, x, block),
+                              lp_row + (x - B.base));
+                continue;
+            }
+            run8_mixed<DT>(P, K, A, &scratch[threadIdx.x >> 6], x, i, B.base, B.base + B.row,
+                           [&](int64_t xt) { return g[xt - x0]; });
+        }
+        __syncthreads();  // the sums are free for the block's next tile
+    }
+}
+
+// Checks of a bucket's index and rows, as zero_reduce_adam_bucket.  rows->n_tile = 0: nothing to do.
+static zero_status bucket_rows(const zero_plan* plan, int64_t b, const void* d_rows, int64_t row_stride,
+                               const char* who, BucketRows* out) {
+    *out = BucketRows{};
+    if (b < 0 || b >= plan->n_buckets) return fail(ZERO_EINVAL, "%s: bucket %lld out of range", who, (long long)b);
+    const int64_t* br = plan->h_bucket + b * kBucketFields;
+    const int64_t base = br[BF_BASE], row = br[BF_ROW], stride = br[BF_STRIDE];
+    if (row == 0) return ZERO_OK;
+    if (!d_rows || !host_aligned16(d_rows)) return fail(ZERO_EINVAL, "%s: rows must be a 16-byte aligned pointer", who);
+    if (row_stride < stride || row_stride % kChunk != 0)
+        return fail(ZERO_EINVAL, "%s: row_stride %lld must be >= %lld and a multiple of 8", who, (long long)row_stride,
+                    (long long)stride);
+    const int64_t tile0 = base >> kTileShift;
+    *out = BucketRows{base, row, stride, tile0, ((base + row + kTileCols - 1) >> kTileShift) - tile0,
+                      static_cast<const uint16_t*>(d_rows), row_stride};
+    return ZERO_OK;
+}
+
+}  // namespace zs
+
+using namespace zs;
+
+extern "C" zero_status zero_reduce_adamw_bucket(const zero_plan* plan, int64_t b, const void* d_rows, int64_t row_stride,
+                                                const uint8_t* d_live, float* d_p32, float* d_m, float* d_v,
+                                                const int32_t* d_flag, void* d_arena, void* d_work, void* stream) {
+    const char* who = "zero_reduce_adamw_bucket";
+    zero_status st = check_device(plan);
+    BucketRows B;
+    if (st != ZERO_OK || (st = bucket_rows(plan, b, d_rows, row_stride, who, &B)) != ZERO_OK || B.n_tile == 0) return st;
+    if (!d_live || !d_p32 || !d_m || !d_v || !d_arena) return fail(ZERO_EINVAL, "%s: NULL pointer", who);
+    if (!host_aligned16(d_p32) || !host_aligned16(d_m) || !host_aligned16(d_v) || !host_aligned16(d_arena))
+        return fail(ZERO_EINVAL, "%s: shard arrays and arena must be 16-byte aligned", who);
+    if ((st = check_work(d_work, who)) != ZERO_OK) return st;
+    const int g = grid_for(B.n_tile);
+    hipStream_t s = (hipStream_t)stream;
+    auto kern = plan->dtype == ZERO_BF16 ? reduce_adamw_kernel<ZERO_BF16> : reduce_adamw_kernel<ZERO_FP16>;
+    kern<<<g, kBlock, 0, s>>>(plan->dev, B, d_live, d_p32, d_m, d_v, work_scal(d_work), work_consts(d_work), d_flag,
+                              static_cast<uint16_t*>(d_arena));
+    return check_launch(who);
+}
+
+extern "C" zero_status zero_reduce_adamw8_bucket(const zero_plan* plan, int64_t b, const void* d_rows,
+                                                 int64_t row_stride, const uint8_t* d_live, float* d_p32,
+                                                 uint8_t* d_m8, uint8_t* d_r8, uint8_t* d_scales,
+                                                 const int32_t* d_flag, void* d_arena, void* d_work, void* stream) {
+    const char* who = "zero_reduce_adamw8_bucket";
+    zero_status st = check_device(plan);
+    BucketRows B;
+    if (st != ZERO_OK || (st = bucket_rows(plan, b, d_rows, row_stride, who, &B)) != ZERO_OK || B.n_tile == 0) return st;
+    if (!d_live || !d_p32 || !d_m8 || !d_r8 || !d_scales || !d_arena) return fail(ZERO_EINVAL, "%s: NULL pointer", who);
+    if (!host_aligned16(d_p32) || !host_aligned16(d_m8) || !host_aligned16(d_r8) || !host_aligned16(d_scales) ||
+        !host_aligned16(d_arena))
+        return fail(ZERO_EINVAL, "%s: shard arrays, scales and arena must be 16-byte aligned", who);
+    if ((st = check_work(d_work, who)) != ZERO_OK) return st;
+    const AdamW8Args A{d_p32, d_m8, d_r8, reinterpret_cast<uint16_t*>(d_scales), d_live, work_scal(d_work),
+                       work_consts(d_work), d_flag, static_cast<uint16_t*>(d_arena)};
+    const int g = grid_for(B.n_tile);
+    auto kern = plan->dtype == ZERO_BF16 ? reduce_adamw8_kernel<ZERO_BF16> : reduce_adamw8_kernel<ZERO_FP16>;
+    kern<<<g, kBlock, 0, (hipStream_t)stream>>>(plan->dev, B, A);
+    return check_launch(who);
+}

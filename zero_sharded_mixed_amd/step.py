@@ -10,6 +10,7 @@ Zero3Schedule issues ZeRO-3's per-layer gathers and reduce-scatters over a plan 
 per layer."""
 from __future__ import annotations
 
+import dataclasses
 from typing import Callable, Optional, Sequence
 
 import torch
@@ -44,6 +45,7 @@ class ShardStep:
         self.packed = torch.zeros(int(s.arena_numel), dtype=torch.int16, device=self.device)
         self.arena = torch.zeros(int(s.arena_numel), dtype=torch.int16, device=self.device)
         self.scaler: Optional[torch.Tensor] = None  # device zero_loss_scaler, once enabled
+        self.adamw_bits = 0  # 32 or 8 once enable_adamw() has been called
 
     def enable_loss_scaler(self, scale: float, growth_interval: int = 2000, growth_factor: float = 2.0,
                            backoff_factor: float = 0.5, min_scale: float = 1.0, max_scale: float = 2.0 ** 24,
@@ -56,6 +58,29 @@ class ShardStep:
 
     def update_loss_scale(self, stream=None) -> None:
         B.zero_loss_scaler_update(self.flag, self.scaler, stream)
+
+    def enable_adamw(self, bits: int = 32) -> None:
+        """Allocate what grad_sumsq(), adamw() and reduce_adamw() use: a workspace of this step's own,
+        the sum of squares and the norm.  bits = 8: the states so far (self.m, self.v) are converted to
+        self.m8, self.r8, self.scales on the current stream and freed; adam() is then refused."""
+        if bits not in (32, 8):
+            raise ValueError("AdamW states have 32 or 8 bits")
+        if self.adamw_bits == 8 and bits == 32:
+            raise ValueError("8-bit states are not converted back")
+        dev = self.device
+        if not self.adamw_bits:
+            self.work = torch.zeros(self.plan.adamw_work_bytes, dtype=torch.uint8, device=dev)
+            self.sumsq = torch.zeros(1, dtype=torch.float64, device=dev)
+            self.norm_out = torch.zeros(2, dtype=torch.float32, device=dev)
+        if bits == 8 and self.adamw_bits != 8:
+            S = int(self.summary.shard_numel)
+            self.m8, self.r8 = (torch.zeros(S, dtype=torch.uint8, device=dev) for _ in range(2))
+            self.scales = torch.zeros(2 * self.plan.adamw_n_scales, dtype=torch.uint8, device=dev)
+            B.zero_adamw8_load(self.plan, self.m, self.v, self.m8, self.r8, self.scales)
+            for t in (self.m, self.v):  # still being read when the references go
+                t.record_stream(torch.cuda.current_stream(dev))
+            self.m = self.v = None
+        self.adamw_bits = bits
 
     # -- views ---------------------------------------------------------------------------
     def block(self, buf: torch.Tensor, b: int) -> torch.Tensor:
@@ -115,6 +140,68 @@ class ShardStep:
             rows, stride = rows_of(b)
             B.zero_reduce_adam_bucket(self.plan, b, rows, stride, self.live, self.p32, self.m, self.v, flag,
                                       self.arena, stream)
+
+    def grad_sumsq(self, check: bool = True, stream=None) -> torch.Tensor:
+        """Sum of squares of the reduced gradient into self.sumsq (this rank's: add the ranks' before
+        adamw()).  check=True: also OR "not finite" into self.flag."""
+        self._need_adamw()
+        B.zero_grad_sumsq(self.plan, self.g32, self.live, self.sumsq, self.work, self.flag if check else None, stream)
+        return self.sumsq
+
+    def _need_adamw(self) -> None:
+        if not self.adamw_bits:
+            raise ValueError("enable_adamw() comes before the first AdamW step")
+
+    def _adamw_params(self, hp: B.AdamWParams) -> B.AdamWParams:
+        """hp with this step's own loss scaler, sum of squares and norm where it names none."""
+        self._need_adamw()
+        own = {}
+        if hp.loss_scaler is None and self.scaler is not None:
+            own["loss_scaler"] = self.scaler
+        if hp.max_norm > 0 and hp.grad_sumsq is None:
+            own["grad_sumsq"] = self.sumsq
+            if hp.norm_out is None:
+                own["norm_out"] = self.norm_out
+        return dataclasses.replace(hp, **own) if own else hp
+
+    def adamw(self, hp: B.AdamWParams, use_flag: bool = True, stream=None) -> None:
+        """One AdamW step on self.g32.  With hp.max_norm > 0 the norm comes from grad_sumsq(), and
+        self.norm_out receives it and the clip coefficient.  A captured graph reads hp's tensors at
+        every replay: keep hp for as long as the graph."""
+        hp, flag = self._adamw_params(hp), self.flag if use_flag else None
+        if self.adamw_bits == 8:
+            B.zero_adamw8_step(self.plan, self.g32, self.p32, self.m8, self.r8, self.scales, self.live, self.steps,
+                               hp, flag, self.arena, self.work, stream)
+        else:
+            B.zero_adamw_step(self.plan, self.g32, self.p32, self.m, self.v, self.live, self.steps, hp, flag,
+                              self.arena, self.work, stream)
+
+    def reduce_adamw(self, rows_of: Callable[[int], tuple], hp: B.AdamWParams, use_flag: bool = True,
+                     stream=None) -> None:
+        """The fused path after pack(check=True), as reduce_adam() with AdamW.  The reduced gradient is
+        not written, so clipping needs a sum of squares that the caller has (hp.grad_sumsq)."""
+        if hp.max_norm > 0 and hp.grad_sumsq is None:
+            raise ValueError("reduce_adamw: clipping needs hp.grad_sumsq (the fused path does not form the norm)")
+        hp, flag = self._adamw_params(hp), self.flag if use_flag else None
+        B.zero_adamw_prepare(self.plan, self.live, self.steps, hp, flag, self.work, stream)
+        for b in range(len(self.buckets)):
+            rows, stride = rows_of(b)
+            if self.adamw_bits == 8:
+                B.zero_reduce_adamw8_bucket(self.plan, b, rows, stride, self.live, self.p32, self.m8, self.r8,
+                                            self.scales, flag, self.arena, self.work, stream)
+            else:
+                B.zero_reduce_adamw_bucket(self.plan, b, rows, stride, self.live, self.p32, self.m, self.v, flag,
+                                           self.arena, self.work, stream)
+
+    def adamw_states(self) -> tuple:
+        """(momentum, root of the variance) that 8-bit states stand for, in bf16 (exact), on the
+        current stream."""
+        if self.adamw_bits != 8:
+            raise ValueError("adamw_states() reads 8-bit states (enable_adamw(8))")
+        m16, r16 = (torch.zeros(int(self.summary.shard_numel), dtype=torch.bfloat16, device=self.device)
+                    for _ in range(2))
+        B.zero_adamw8_unload(self.plan, self.m8, self.r8, self.scales, m16, r16)
+        return m16, r16
 
     def unpack(self, param_ptrs: torch.Tensor, src: Optional[torch.Tensor] = None, stream=None) -> None:
         src = self.arena if src is None else src
