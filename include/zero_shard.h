@@ -481,7 +481,7 @@ zero_status zero_adamw_get_sizes(const zero_plan* plan, zero_adamw_sizes* out);
 typedef struct zero_adamw_hparams {
     double lr;                            /* >= 0                                          */
     double beta1, beta2;                  /* in [0, 1)                                     */
-    double eps;                           /* > 0 in fp32                                   */
+    double eps;                           /* finite, >= 2^-126                             */
     double weight_decay;                  /* >= 0                                          */
     double grad_scale;                    /* as zero_adam_hparams                          */
     double max_norm;                      /* >= 0; 0 = no clipping; > 0 needs grad_sumsq   */

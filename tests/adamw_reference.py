@@ -93,9 +93,9 @@ def encode(x, idx, on, n_scales, kind, h=None):
     if h is None:
         up = (share > 0.5) | ((share == 0.5) & (k % 2 == 1))
     else:
-        # fp32 holds the share in `bits` bits below the code (all of them zero in a code's own
-        # subnormals, where the value is rounded to that grid first)
-        part = np.rint(share * 2.0 ** bits).astype(np.int64)
+        # a share has `bits` bits below the code, more only among the code's subnormals, where r's is
+        # rounded to that many first
+        part = share * 2.0 ** bits if kind == "m" else np.rint(share * 2.0 ** bits)
         r = (((h & np.uint64(0xFFFF)).astype(np.int64) << 4) + 8) if kind == "m" else \
             (((h >> np.uint64(16)).astype(np.int64) << 3) + 4)
         up = part + r >= 1 << bits
@@ -129,9 +129,12 @@ class Step:
         self.shrink = lr * g("weight_decay", 0.0) * d
 
 
-def adamw64(st: Step, i, g32, p, m, v):
+def adamw64(st: Step, i, g32, p, m, v, estimates=False):
     """New (p, m, v) of columns whose parameters are i, in 64 bits, and how far fp32 may be off each:
-    every operation rounds by at most U relative, and a scalar rounded once carries U."""
+    every operation rounds by at most U relative, and a scalar rounded once carries U.  estimates (the
+    8-bit step): the root and the reciprocal may be off by a unit in the last place, 2 U, and the
+    quotient is a product besides."""
+    unit = 2 if estimates else 1
     with np.errstate(all="ignore"):
         g = g32.astype(np.float64) * st.mult                      # the scalar, the product: 2 U
         bm, cg = st.b1 * m, (1 - st.b1) * g
@@ -141,11 +144,12 @@ def adamw64(st: Step, i, g32, p, m, v):
         v1 = bv + cg2
         ev = U * (2 * bv + 7 * cg2 + v1)                          # g^2: 2 * 2 U + U; 1-beta U, product U; sum U
         root = np.sqrt(v1)
-        er = ev / (2 * np.where(root > 0, root, 1)) + U * root
+        er = ev / (2 * np.where(root > 0, root, 1)) + unit * U * root
         den = root * st.rbc2[i] + st.eps
         ed = er * st.rbc2[i] + U * (2 * root * st.rbc2[i] + st.eps + den)
         up = st.step[i] * m1 / den
-        eu = st.step[i] * em / den + abs(up) * (ed / den + 3 * U)  # quotient U, step U, product U
+        quotient = 3 if estimates else 1                          # reciprocal 2 U and product U, or U
+        eu = st.step[i] * em / den + abs(up) * (ed / den + (quotient + 2) * U)  # and step U, product U
         sh = st.shrink[i] * p
         p1 = p - sh - up
         ep = 2 * U * abs(sh) + eu + U * (abs(p - sh) + abs(p1))

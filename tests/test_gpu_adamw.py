@@ -323,7 +323,7 @@ def test_adamw8_step(name, dtype):
     st.adamw(hp)
     own = np.maximum(c.own, 0)
     ref = c.ref(hp)
-    (p, m, v), (ep, em, ev) = R.adamw64(ref, own, c.g, c.p.astype(np.float64), m0, r0 * r0)
+    (p, m, v), (ep, em, ev) = R.adamw64(ref, own, c.g, c.p.astype(np.float64), m0, r0 * r0, True)
     check_parameters(c, st, p, ep, name)
     gm, gr, gs = codes(st)
     # bit for bit
@@ -519,7 +519,8 @@ def test_a_run_of_steps_as_a_program_takes_them(bits):
                               grad_scale=hp.grad_scale, max_norm=hp.max_norm, decay=c.decay, scale=scale,
                               sumsq=math.fsum(float(x) ** 2 for x in before["g32"][c.on])),
                          before["steps"] + c.live, c.n)
-            (p, _, _), (ep, _, _) = R.adamw64(ref, own, before["g32"], before["p32"].astype(np.float64), m0, v0)
+            (p, _, _), (ep, _, _) = R.adamw64(ref, own, before["g32"], before["p32"].astype(np.float64), m0, v0,
+                                           bits == 8)
             close(host(st.p32), p, ep, c.on, f"step {k}")
             assert abs(float(st.norm_out[1]) - ref.coef) <= 2 * R.U * ref.coef
         st.update_loss_scale()
@@ -648,7 +649,7 @@ def test_columns_past_two_to_the_32():
         got = host(scales[first:first + idx.max() + 1])
         used = np.unique(idx)
         assert np.array_equal(got[used], np.stack([bm, br], 1)[used])
-        (pw, _, _), (ep, _, _) = R.adamw64(ref, own, x, np.zeros(k), np.zeros(k), np.zeros(k))
+        (pw, _, _), (ep, _, _) = R.adamw64(ref, own, x, np.zeros(k), np.zeros(k), np.zeros(k), True)
         close(host(p[a:a + k]), pw, ep, np.ones(k, bool), "p32")
     mid = slice(1 << 31, (1 << 31) + 100000)
     assert not p[mid].any() and not m8[mid].any()
@@ -661,7 +662,7 @@ def test_refused_calls_change_nothing():
     st = c.reset()
     before = [t.clone() for t in (st.p32, st.m, st.v, st.steps, st.arena)]
     for bad in (dict(lr=-1.0), dict(lr=float("nan")), dict(beta1=1.0), dict(beta2=-0.1), dict(eps=0.0),
-                dict(eps=1e-60), dict(eps=float("inf")), dict(weight_decay=-0.1), dict(weight_decay=float("inf")),
+                dict(eps=1e-60), dict(eps=1e-39), dict(eps=float("inf")), dict(weight_decay=-0.1), dict(weight_decay=float("inf")),
                 dict(grad_scale=float("nan")), dict(max_norm=-1.0), dict(max_norm=float("nan"))):
         with pytest.raises(Z.ZeroError) as e:
             st.adamw(c.hp(**bad))

@@ -9,6 +9,15 @@
 
 #include "zs_adamw.h"
 
+#ifndef LOADS_FIRST
+#define LOADS_FIRST
+#endif
+#ifndef AB
+#define AB 1
+#endif
+#ifndef ALDS
+#define ALDS 0
+#endif
 namespace zs {
 
 // First column of the run that pass q of a block's tile gives the wavefront's lane, and its own.
@@ -17,51 +26,42 @@ __device__ __forceinline__ int64_t run_of(int64_t x) { return x & ~(kRun - 1); }
 template <int DT>
 __global__ __launch_bounds__(kBlock) void adamw8_kernel(DevPlan P, AdamW8Args A, const float* __restrict__ g32) {
     if (A.flag && *A.flag) return;
+    __shared__ TileMap map;
     __shared__ RunMax scratch[kBlock / 64];
     const AdamK K = load_adam_consts(A.consts);
     for (int64_t j = blockIdx.x; j < P.n_tiles; j += gridDim.x) {
-        const int64_t x0 = j << kTileShift;
-        const int64_t iu = ld_const(P.tile_first, j);
-        const int64_t ic = iu < P.n ? iu : P.n - 1;
-        if (iu < P.n && ld_const(P.off, ic) <= x0 && ld_const(P.end, ic) >= x0 + kTileCols) {
-            if (!ld_const(A.live, ic)) continue;
-            const AdamWScal s = ld_const_scal(A.scal, ic);
-            const int32_t b = ld_const(P.bucket, ic);
-            const int64_t O = ld_const(P.b_base, b);
-            uint16_t* lp = A.arena + P.nd * O + P.rank * ld_const(P.b_stride, b) + (x0 - O);
-            float4 g[2];
-            Run8 r[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int64_t x = x0 + quad_col(q);
-                g[q] = load4f_nt(g32 + x);
-                r[q] = run8_load(A, x, (x >> kRunShift) + ic);
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int64_t x = x0 + quad_col(q);
-                run8_step<DT>(K, s, A, x, (x >> kRunShift) + ic, g[q], r[q], lp + quad_col(q));
-            }
+        const Tile T(P, A.scal, j);
+        if (T.whole) {
+            if (!T.s.live()) continue;
+            uint16_t* lp = A.arena + T.row(P);
+            const int64_t xa = T.x0 + quad_col(0), xb = T.x0 + quad_col(1);
+            const int64_t block = (xa >> kRunShift) + T.first;
+            const float4 ga = load4f_nt(g32 + xa);
+            Run8 a = run8_load(A, xa);
+            a.scale = gptr(A.scales)[block];
+            const Out8 oa = run8_math(K, T.s, xa, ga, a);
+            __builtin_amdgcn_sched_barrier(0);
+            const float4 gb = load4f_nt(g32 + xb);
+            Run8 b = run8_load(A, xb);
+            b.scale = gptr(A.scales)[block + ((xb - xa) >> kRunShift)];
+            __builtin_amdgcn_sched_barrier(0);
+            run8_store<DT>(A, xa, block, a.p, oa, lp + quad_col(0));
+            __builtin_amdgcn_sched_barrier(0);
+            const Out8 ob = run8_math(K, T.s, xb, gb, b);
+            run8_store<DT>(A, xb, block + ((xb - xa) >> kRunShift), b.p, ob, lp + quad_col(1));
             continue;
         }
+        mixed_tile(map, P, A.scal, T, j, [&](int64_t first) {
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-            const int64_t x = x0 + quad_col(q);
-            const int64_t run = run_of(x);
-            if (run >= P.shard_numel) break;
-            const int64_t i = param_of_column(P, x);
-            // a parameter that covers the run is the one that every lane found
-            if (i < P.n && P.off[i] <= run && P.end[i] >= run + kRun) {
-                if (!A.live[i]) continue;
-                const int32_t b = P.bucket[i];
-                const int64_t O = P.b_base[b], block = (run >> kRunShift) + i;
-                run8_step<DT>(K, scal_of(A.scal[i]), A, x, block, load4f_nt(g32 + x), run8_load(A, x, block),
-                              A.arena + P.nd * O + P.rank * P.b_stride[b] + (x - O));
-                continue;
+            for (int q = 0; q < 2; ++q) {
+                const int64_t x = T.x0 + quad_col(q);
+                if (run_of(x) >= P.shard_numel) break;
+                const bool in = x < P.shard_numel;
+                const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                run8_mixed<DT>(map, K, A, &scratch[threadIdx.x >> 6], first, x, int(quad_col(q)), in,
+                               in ? load4f_nt(g32 + x) : none, in ? run8_load(A, x) : Run8{none, 0, 0, 0});
             }
-            run8_mixed<DT>(P, K, A, &scratch[threadIdx.x >> 6], x, i, 0, P.shard_numel,
-                           [&](int64_t xt) { return gptr(g32)[xt]; });
-        }
+        });
     }
 }
 
@@ -108,8 +108,8 @@ __global__ __launch_bounds__(kBlock) void adamw8_load_kernel(DevPlan P, const fl
                 if (own[t] < 0) continue;
                 const int64_t xt = x + t;
                 const uint32_t mb = moment_byte(S->m[first[t]]), rb = root_byte(S->r[first[t]]);
-                gptr(m8)[xt] = mb == kScaleNan ? 0 : uint8_t(moment_code_near(m[t], inverse_of_byte(mb)));
-                gptr(r8)[xt] = rb == kScaleNan ? 0 : uint8_t(root_code_near(r[t], inverse_of_byte(rb)));
+                gptr(m8)[xt] = mb == kScaleNan ? 0 : uint8_t(moment_near(m[t], mb));
+                gptr(r8)[xt] = rb == kScaleNan ? 0 : uint8_t(root_near(r[t], rb));
                 if (l4 + t == first[t]) gptr(scales)[(run >> kRunShift) + own[t]] = uint16_t(mb | (rb << 8));
             }
             wave_lds_fence();
@@ -117,45 +117,58 @@ __global__ __launch_bounds__(kBlock) void adamw8_load_kernel(DevPlan P, const fl
     }
 }
 
-// The states' values in bf16, which holds them exactly: 2 bytes in and 4 out per element.
-__device__ __forceinline__ uint32_t bf16_bits(float f) { return __float_as_uint(f) >> 16; }
-__device__ __forceinline__ uint64_t bf16x4(const float (&f)[4]) {
-    return uint64_t(bf16_bits(f[0]) | (bf16_bits(f[1]) << 16)) | uint64_t(bf16_bits(f[2]) | (bf16_bits(f[3]) << 16)) << 32;
+// The states' values in bf16, which holds them exactly: 2 bytes in and 4 out per element.  8
+// columns in a row per thread: 8-byte loads and 16-byte stores of whole lines.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    return (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xffff0000u);
+}
+__device__ __forceinline__ void unload8(const uint8_t* m8, const uint8_t* r8, uint32_t pair, uint16_t* m16,
+                                        uint16_t* r16) {
+    const float ms = pow2_of_byte(pair & 0xffu);
+    const uint64_t mw = __builtin_nontemporal_load(gptr(reinterpret_cast<const uint64_t*>(m8)));
+    const uint64_t rw = __builtin_nontemporal_load(gptr(reinterpret_cast<const uint64_t*>(r8)));
+    float lo[4], hi[4];
+    moment_values(uint32_t(mw), lo);
+    moment_values(uint32_t(mw >> 32), hi);
+    const uint32_t m[4] = {bf16_pair(lo[0] * ms, lo[1] * ms), bf16_pair(lo[2] * ms, lo[3] * ms),
+                           bf16_pair(hi[0] * ms, hi[1] * ms), bf16_pair(hi[2] * ms, hi[3] * ms)};
+    uint32_t r[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        r[t] = bf16_pair(root_value(uint32_t(rw >> (16 * t)) & 0xffu, pair >> 8),
+                         root_value(uint32_t(rw >> (16 * t + 8)) & 0xffu, pair >> 8));
+    store16(m16, make_uint4(m[0], m[1], m[2], m[3]));
+    store16(r16, make_uint4(r[0], r[1], r[2], r[3]));
 }
 __global__ __launch_bounds__(kBlock) void adamw8_unload_kernel(DevPlan P, const uint8_t* __restrict__ m8,
                                                                const uint8_t* __restrict__ r8,
                                                                const uint16_t* __restrict__ scales,
                                                                uint16_t* __restrict__ m16, uint16_t* __restrict__ r16) {
     for (int64_t j = blockIdx.x; j < P.n_tiles; j += gridDim.x) {
+        const int64_t x0 = j << kTileShift;
+        const int64_t x = x0 + int64_t(threadIdx.x) * kChunk;
+        const int64_t iu = ld_const(P.tile_first, j);
+        const int64_t ic = iu < P.n ? iu : P.n - 1;
+        if (iu < P.n && ld_const(P.off, ic) <= x0 && ld_const(P.end, ic) >= x0 + kTileCols) {
+            unload8(m8 + x, r8 + x, gptr(scales)[(x >> kRunShift) + ic], m16 + x, r16 + x);
+            continue;
+        }
+        if (x >= P.shard_numel) continue;
+        int64_t i = param_of_column(P, x);
+        if (i < P.n && P.off[i] <= x && x + kChunk <= P.end[i]) {
+            unload8(m8 + x, r8 + x, gptr(scales)[(x >> kRunShift) + i], m16 + x, r16 + x);
+            continue;
+        }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int64_t x = (j << kTileShift) + quad_col(q);
-            if (x >= P.shard_numel) break;
-            int64_t i = param_of_column(P, x);
-            if (i < P.n && P.off[i] <= x && x + 4 <= P.end[i]) {
-                const uint32_t pair = gptr(scales)[(x >> kRunShift) + i];
-                const float ms = pow2_of_byte(pair & 0xffu), rs = pow2_of_byte(pair >> 8);
-                const uint32_t mw = *gptr(reinterpret_cast<const uint32_t*>(m8 + x));
-                const uint32_t rw = *gptr(reinterpret_cast<const uint32_t*>(r8 + x));
-                float m[4], r[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    m[t] = moment_value((mw >> (8 * t)) & 0xffu) * ms;
-                    r[t] = root_value((rw >> (8 * t)) & 0xffu) * rs;
-                }
-                store8(m16 + x, bf16x4(m));
-                store8(r16 + x, bf16x4(r));
-                continue;
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int64_t xt = x + t;
-                while (i < P.n && P.end[i] <= xt) ++i;
-                if (!(i < P.n && P.off[i] <= xt)) continue;
-                const uint32_t pair = gptr(scales)[(x >> kRunShift) + i];
-                gptr(m16)[xt] = uint16_t(bf16_bits(moment_value(gptr(m8)[xt]) * pow2_of_byte(pair & 0xffu)));
-                gptr(r16)[xt] = uint16_t(bf16_bits(root_value(gptr(r8)[xt]) * pow2_of_byte(pair >> 8)));
-            }
+        for (int t = 0; t < kChunk; ++t) {
+            const int64_t xt = x + t;
+            while (i < P.n && P.end[i] <= xt) ++i;
+            if (!(i < P.n && P.off[i] <= xt)) continue;
+            const uint32_t pair = gptr(scales)[(x >> kRunShift) + i];
+            float m[4];
+            moment_values(gptr(m8)[xt], m);
+            gptr(m16)[xt] = uint16_t(bf16_pair(m[0] * pow2_of_byte(pair & 0xffu), 0.0f));
+            gptr(r16)[xt] = uint16_t(bf16_pair(root_value(gptr(r8)[xt], pair >> 8), 0.0f));
         }
     }
 }
@@ -179,7 +192,7 @@ extern "C" zero_status zero_adamw8_step(const zero_plan* plan, const float* d_g3
     hipStream_t s = (hipStream_t)stream;
     if ((st = launch_adamw_prepare(plan, d_live, d_steps, hp, d_flag, d_work, s, who)) != ZERO_OK) return st;
     if (plan->shard_numel == 0) return ZERO_OK;
-    const AdamW8Args A{d_p32, d_m8, d_r8, reinterpret_cast<uint16_t*>(d_scales), d_live, work_scal(d_work),
+    const AdamW8Args A{d_p32, d_m8, d_r8, reinterpret_cast<uint16_t*>(d_scales), work_scal(d_work),
                        work_consts(d_work), d_flag, static_cast<uint16_t*>(d_arena)};
     const int g = grid_for(plan->dev.n_tiles);
     if (plan->dtype == ZERO_BF16) adamw8_kernel<ZERO_BF16><<<g, kBlock, 0, s>>>(plan->dev, A, d_g32);

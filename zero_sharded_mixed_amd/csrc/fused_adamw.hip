@@ -7,13 +7,30 @@
 
 namespace zs {
 
+// Row forms (zs_common.h) and blocks per CU, by the number of rows and the states' bits, measured on
+// MI355X as the time of a step's launches: the GPT-2 list at Nd = 8, the 7.5B list at Nd = 64 and the
+// ragged list at Nd = 1024.
+//   32 bits, Nd >= kManyRows: fewest registers on whole tiles, two groups of rows in flight on the
+//     others (180 registers, two waves per SIMD): 3.28 ms and 0.82 ms; with one group on the others
+//     (five waves) 3.45 and 0.85;
+//   32 bits below: one group on the others, at four blocks per CU: 1.36 ms; 1.40 at five, 1.75 with
+//     two groups;
+//   8 bits, Nd >= kManyRows: the same, at three blocks per CU: 3.05 ms and 0.83 ms; 3.15 and 0.83 at
+//     five, 3.17 and 0.80 with two groups;
+//   8 bits below: a group of rows at once on whole tiles too, five blocks: 1.02 ms; 1.07 with fewest
+//     registers, 1.23 at three blocks.
+constexpr int64_t kManyRows = 16;
+// Reserved where fewer blocks are faster: with the kernels' own 16 and 24 KB, four and three blocks
+// fit a CU's 160 KB.
+constexpr unsigned kFewBlocksLds = 16 * 1024;
+
 // A tile inside one live parameter: every thread sums 8 columns in a row (16-byte loads of every
 // rank's row), the sums go through LDS, and the step takes the tile lane-strided.  The tile's
 // reduced gradient as the thread's two quads:
-template <int DT>
+template <int DT, int FORM>
 __device__ __forceinline__ void tile_sums(float4* g_lds, const uint16_t* rows_u, int64_t nd, int64_t row_stride) {
     float acc[8];
-    reduce_rows8<DT, kRowsLow, true>(rows_u, threadIdx.x * kChunk, nd, row_stride, acc);
+    reduce_rows8<DT, FORM, true>(rows_u, threadIdx.x * kChunk, nd, row_stride, acc);
     g_lds[2 * threadIdx.x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     g_lds[2 * threadIdx.x + 1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
 }
@@ -24,7 +41,21 @@ struct BucketRows {
     int64_t row_stride;
 };
 
-template <int DT>
+// The other tiles: the sums of the 8-column groups that hold a live column of the bucket.  The rest
+// of the LDS is left as it was: those sums belong to nobody.
+template <int DT, int FORM>
+__device__ __forceinline__ void mixed_sums(float4* g_lds, const DevPlan& P, const BucketRows& B,
+                                           const uint8_t* __restrict__ live, int64_t x0) {
+    const int64_t x = x0 + int64_t(threadIdx.x) * kChunk;
+    const int64_t c = x - B.base;
+    if (c < 0 || c >= B.row || live_mask8(P, live, x, param_of_column(P, x)) == 0) return;
+    float acc[8];
+    reduce_rows8<DT, FORM, true>(B.rows + (x0 - B.base), threadIdx.x * kChunk, P.nd, B.row_stride, acc);
+    g_lds[2 * threadIdx.x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    g_lds[2 * threadIdx.x + 1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+}
+
+template <int DT, int WHOLE, int MIXED>
 __global__ __launch_bounds__(kBlock) void reduce_adamw_kernel(DevPlan P, BucketRows B, const uint8_t* __restrict__ live,
                                                               float* __restrict__ p32, float* __restrict__ m,
                                                               float* __restrict__ v, const float4* __restrict__ scal,
@@ -33,21 +64,19 @@ __global__ __launch_bounds__(kBlock) void reduce_adamw_kernel(DevPlan P, BucketR
                                                               uint16_t* __restrict__ arena) {
     if (flag && *flag) return;
     __shared__ float4 g_lds[kTileCols / 4];
+    __shared__ TileMap map;
     const AdamK K = load_adam_consts(consts);
     uint16_t* const lp_row = arena + P.nd * B.base + P.rank * B.stride;  // row r of the bucket's block
     for (int64_t w = blockIdx.x; w < B.n_tile; w += gridDim.x) {
         const int64_t j = B.tile0 + w;
-        const int64_t x0 = j << kTileShift;
-        const int64_t iu = ld_const(P.tile_first, j);
-        const int64_t ic = iu < P.n ? iu : P.n - 1;
-        if (iu < P.n && ld_const(P.off, ic) <= x0 && ld_const(P.end, ic) >= x0 + kTileCols) {
-            if (!ld_const(live, ic)) continue;
-            const AdamWScal s = ld_const_scal(scal, ic);
-            tile_sums<DT>(g_lds, B.rows + (x0 - B.base), P.nd, B.row_stride);
+        const Tile T(P, scal, j);
+        if (T.whole) {
+            if (!T.s.live()) continue;
+            tile_sums<DT, WHOLE>(g_lds, B.rows + (T.x0 - B.base), P.nd, B.row_stride);
             float4 p4[2], m4[2], v4[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int64_t x = x0 + quad_col(q);
+                const int64_t x = T.x0 + quad_col(q);
                 p4[q] = load4f_nt(p32 + x);
                 m4[q] = load4f_nt(m + x);
                 v4[q] = load4f_nt(v + x);
@@ -59,66 +88,45 @@ __global__ __launch_bounds__(kBlock) void reduce_adamw_kernel(DevPlan P, BucketR
             __syncthreads();  // the LDS is free for the block's next tile
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int64_t x = x0 + quad_col(q);
-                adamw_quad<DT>(K, s, g4[q], p4[q], m4[q], v4[q], p32 + x, m + x, v + x, lp_row + (x - B.base));
+                const int64_t x = T.x0 + quad_col(q);
+                adamw_quad<DT>(K, T.s, g4[q], p4[q], m4[q], v4[q], p32 + x, m + x, v + x, lp_row + (x - B.base));
             }
             continue;
         }
-        const int64_t x = x0 + int64_t(threadIdx.x) * kChunk;
-        const int64_t c = x - B.base;
-        if (c < 0 || c >= B.row) continue;  // outside the bucket, or entirely in the row gap
-        int64_t i = param_of_column(P, x);
-        const unsigned mask = live_mask8(P, live, x, i);
-        if (mask == 0) continue;
-        float acc[8];
-        reduce_rows8<DT, kRowsPipe, true>(B.rows + (x0 - B.base), threadIdx.x * kChunk, P.nd, B.row_stride, acc);
-        if (mask == 0xffu && i < P.n && P.off[i] <= x && x + kChunk <= P.end[i]) {
-            const AdamWScal s = scal_of(scal[i]);
-#pragma unroll
+        mixed_sums<DT, MIXED>(g_lds, P, B, live, T.x0);
+        mixed_tile(map, P, scal, T, j, [&](int64_t) {
+#pragma unroll 1
             for (int q = 0; q < 2; ++q) {
-                const int64_t xq = x + 4 * q;
-                adamw_quad<DT>(K, s, make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]),
-                               load4f(p32 + xq), load4f(m + xq), load4f(v + xq), p32 + xq, m + xq, v + xq,
-                               lp_row + c + 4 * q);
+                const int64_t x = T.x0 + quad_col(q);
+                if (x >= B.base && x < B.base + B.row)
+                    adamw_quad_mixed<DT>(map, K, int(quad_col(q)), g_lds[quad_col(q) / 4], load4f_nt(p32 + x),
+                                         load4f_nt(m + x), load4f_nt(v + x), p32 + x, m + x, v + x, arena);
             }
-            continue;
-        }
-#pragma unroll
-        for (int t = 0; t < kChunk; ++t) {
-            if (!(mask & (1u << t))) continue;
-            const int64_t xt = x + t;
-            while (i < P.n && P.end[i] <= xt) ++i;
-            float pe = gptr(p32)[xt], me = gptr(m)[xt], ve = gptr(v)[xt];
-            adamw_elem(K, scal_of(scal[i]), acc[t], pe, me, ve);
-            gptr(p32)[xt] = pe;
-            gptr(m)[xt] = me;
-            gptr(v)[xt] = ve;
-            gptr(lp_row)[c + t] = from_f32<DT>(pe);
-        }
+        });
     }
 }
 
-template <int DT>
-__global__ __launch_bounds__(kBlock) void reduce_adamw8_kernel(DevPlan P, BucketRows B, AdamW8Args A) {
+template <int DT, int WHOLE, int MIXED>
+__global__ __launch_bounds__(kBlock) void reduce_adamw8_kernel(DevPlan P, BucketRows B, const uint8_t* __restrict__ live,
+                                                               AdamW8Args A) {
     if (A.flag && *A.flag) return;
     __shared__ float4 g_lds[kTileCols / 4];
+    __shared__ TileMap map;
     __shared__ RunMax scratch[kBlock / 64];
     const AdamK K = load_adam_consts(A.consts);
     uint16_t* const lp_row = A.arena + P.nd * B.base + P.rank * B.stride;
     for (int64_t w = blockIdx.x; w < B.n_tile; w += gridDim.x) {
         const int64_t j = B.tile0 + w;
-        const int64_t x0 = j << kTileShift;
-        const int64_t iu = ld_const(P.tile_first, j);
-        const int64_t ic = iu < P.n ? iu : P.n - 1;
-        if (iu < P.n && ld_const(P.off, ic) <= x0 && ld_const(P.end, ic) >= x0 + kTileCols) {
-            if (!ld_const(A.live, ic)) continue;
-            const AdamWScal s = ld_const_scal(A.scal, ic);
-            tile_sums<DT>(g_lds, B.rows + (x0 - B.base), P.nd, B.row_stride);
+        const Tile T(P, A.scal, j);
+        if (T.whole) {
+            if (!T.s.live()) continue;
+            tile_sums<DT, WHOLE>(g_lds, B.rows + (T.x0 - B.base), P.nd, B.row_stride);
             Run8 r[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int64_t x = x0 + quad_col(q);
-                r[q] = run8_load(A, x, (x >> kRunShift) + ic);
+                const int64_t x = T.x0 + quad_col(q);
+                r[q] = run8_load(A, x);
+                r[q].scale = gptr(A.scales)[(x >> kRunShift) + T.first];
             }
             __syncthreads();
             float4 g4[2];
@@ -127,42 +135,24 @@ __global__ __launch_bounds__(kBlock) void reduce_adamw8_kernel(DevPlan P, Bucket
             __syncthreads();
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int64_t x = x0 + quad_col(q);
-                run8_step<DT>(K, s, A, x, (x >> kRunShift) + ic, g4[q], r[q], lp_row + (x - B.base));
+                const int64_t x = T.x0 + quad_col(q);
+                run8_step<DT>(K, T.s, A, x, (x >> kRunShift) + T.first, g4[q], r[q], lp_row + (x - B.base));
             }
             continue;
         }
-        // The other tiles: the bucket's live columns are summed into the LDS as above (the rest of
-        // it is not read), then every wavefront takes its two runs.
-        {
-            const int64_t x = x0 + int64_t(threadIdx.x) * kChunk;
-            const int64_t c = x - B.base;
-            if (c >= 0 && c < B.row && live_mask8(P, A.live, x, param_of_column(P, x)) != 0) {
-                float acc[8];
-                reduce_rows8<DT, kRowsPipe, true>(B.rows + (x0 - B.base), threadIdx.x * kChunk, P.nd, B.row_stride, acc);
-                g_lds[2 * threadIdx.x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                g_lds[2 * threadIdx.x + 1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-            }
-        }
-        __syncthreads();
-        const float* g = reinterpret_cast<const float*>(g_lds);
+        mixed_sums<DT, MIXED>(g_lds, P, B, live, T.x0);
+        mixed_tile(map, P, A.scal, T, j, [&](int64_t first) {
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-            const int64_t x = x0 + quad_col(q);
-            const int64_t run = x & ~(kRun - 1);
-            if (run >= B.base + B.row || run + kRun <= B.base) continue;
-            const int64_t i = param_of_column(P, x);
-            if (i < P.n && P.off[i] <= run && P.end[i] >= run + kRun) {
-                if (!A.live[i]) continue;
-                const int64_t block = (run >> kRunShift) + i;
-                run8_step<DT>(K, scal_of(A.scal[i]), A, x, block, g_lds[quad_col(q) / 4], run8_load(A, x, block),
-                              lp_row + (x - B.base));
-                continue;
+            for (int q = 0; q < 2; ++q) {
+                const int64_t x = T.x0 + quad_col(q);
+                const int64_t run = x & ~(kRun - 1);
+                if (run >= B.base + B.row || run + kRun <= B.base) continue;
+                const bool in = x >= B.base && x < B.base + B.row;
+                run8_mixed<DT>(map, K, A, &scratch[threadIdx.x >> 6], first, x, int(quad_col(q)), in,
+                               g_lds[quad_col(q) / 4],
+                               in ? run8_load(A, x) : Run8{make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0, 0, 0});
             }
-            run8_mixed<DT>(P, K, A, &scratch[threadIdx.x >> 6], x, i, B.base, B.base + B.row,
-                           [&](int64_t xt) { return g[xt - x0]; });
-        }
-        __syncthreads();  // the sums are free for the block's next tile
+        });
     }
 }
 
@@ -201,8 +191,11 @@ extern "C" zero_status zero_reduce_adamw_bucket(const zero_plan* plan, int64_t b
     if ((st = check_work(d_work, who)) != ZERO_OK) return st;
     const int g = grid_for(B.n_tile);
     hipStream_t s = (hipStream_t)stream;
-    auto kern = plan->dtype == ZERO_BF16 ? reduce_adamw_kernel<ZERO_BF16> : reduce_adamw_kernel<ZERO_FP16>;
-    kern<<<g, kBlock, 0, s>>>(plan->dev, B, d_live, d_p32, d_m, d_v, work_scal(d_work), work_consts(d_work), d_flag,
+    const bool big = plan->nd >= kManyRows;
+    auto kern = plan->dtype == ZERO_BF16
+                    ? (big ? reduce_adamw_kernel<ZERO_BF16, kRowsLow, kRowsPipe> : reduce_adamw_kernel<ZERO_BF16, kRowsLow, kRowsGroup>)
+                    : (big ? reduce_adamw_kernel<ZERO_FP16, kRowsLow, kRowsPipe> : reduce_adamw_kernel<ZERO_FP16, kRowsLow, kRowsGroup>);
+    kern<<<g, kBlock, big ? 0u : kFewBlocksLds, s>>>(plan->dev, B, d_live, d_p32, d_m, d_v, work_scal(d_work), work_consts(d_work), d_flag,
                               static_cast<uint16_t*>(d_arena));
     return check_launch(who);
 }
@@ -220,10 +213,13 @@ extern "C" zero_status zero_reduce_adamw8_bucket(const zero_plan* plan, int64_t 
         !host_aligned16(d_arena))
         return fail(ZERO_EINVAL, "%s: shard arrays, scales and arena must be 16-byte aligned", who);
     if ((st = check_work(d_work, who)) != ZERO_OK) return st;
-    const AdamW8Args A{d_p32, d_m8, d_r8, reinterpret_cast<uint16_t*>(d_scales), d_live, work_scal(d_work),
+    const AdamW8Args A{d_p32, d_m8, d_r8, reinterpret_cast<uint16_t*>(d_scales), work_scal(d_work),
                        work_consts(d_work), d_flag, static_cast<uint16_t*>(d_arena)};
     const int g = grid_for(B.n_tile);
-    auto kern = plan->dtype == ZERO_BF16 ? reduce_adamw8_kernel<ZERO_BF16> : reduce_adamw8_kernel<ZERO_FP16>;
-    kern<<<g, kBlock, 0, (hipStream_t)stream>>>(plan->dev, B, A);
+    const bool big = plan->nd >= kManyRows;
+    auto kern = plan->dtype == ZERO_BF16
+                    ? (big ? reduce_adamw8_kernel<ZERO_BF16, kRowsLow, kRowsGroup> : reduce_adamw8_kernel<ZERO_BF16, kRowsGroup, kRowsGroup>)
+                    : (big ? reduce_adamw8_kernel<ZERO_FP16, kRowsLow, kRowsGroup> : reduce_adamw8_kernel<ZERO_FP16, kRowsGroup, kRowsGroup>);
+    kern<<<g, kBlock, big ? kFewBlocksLds : 0u, (hipStream_t)stream>>>(plan->dev, B, d_live, A);
     return check_launch(who);
 }

@@ -31,10 +31,12 @@ inline double* work_parts(void* w, int64_t n) {
 
 // One parameter's scalars of a step, formed in double and rounded to fp32 once: step size
 // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t), lr * weight_decay * d, and the 32-bit key of the
-// 8-bit states' rounding noise.
+// 8-bit states' rounding noise.  The second is at least 1, and 0 for a parameter without a
+// gradient: one load tells a step's kernels both.
 struct AdamWScal {
     float step, inv_sqrt_bc2, shrink;
     uint32_t key;
+    __device__ __forceinline__ bool live() const { return inv_sqrt_bc2 != 0.0f; }
 };
 __device__ __forceinline__ AdamWScal scal_of(const float4& f) {
     return AdamWScal{f.x, f.y, f.z, __float_as_uint(f.w)};
@@ -44,6 +46,81 @@ __device__ __forceinline__ AdamWScal ld_const_scal(const float4* p, int64_t i) {
     const float* f = reinterpret_cast<const float*>(p + i);
     return AdamWScal{ld_const(f, 0), ld_const(f, 1), ld_const(f, 2), __float_as_uint(ld_const(f, 3))};
 }
+
+// A tile, block-uniform: its first column, the first parameter whose range ends after it, whether
+// that parameter covers the whole tile, its scalars, and the arena index of the tile's first column
+// in its row.  All loaded at once, so that they cost two memory round trips, not one each.
+struct Tile {
+    int64_t x0, first;
+    bool whole;
+    AdamWScal s;
+    int32_t bucket;
+    __device__ __forceinline__ Tile(const DevPlan& P, const float4* scal, int64_t j) {
+        x0 = j << kTileShift;
+        first = ld_const(P.tile_first, j);
+        const int64_t ic = first < P.n ? first : P.n - 1;
+        const int64_t off = ld_const(P.off, ic), end = ld_const(P.end, ic);
+        s = ld_const_scal(scal, ic);
+        bucket = ld_const(P.bucket, ic);
+        whole = (first < P.n) & (off <= x0) & (end >= x0 + kTileCols);
+    }
+    __device__ __forceinline__ int64_t row(const DevPlan& P) const {
+        const int64_t O = ld_const(P.b_base, bucket);
+        return P.nd * O + P.rank * ld_const(P.b_stride, bucket) + (x0 - O);
+    }
+};
+
+// ------------------------------------------------------- the parameters of a mixed tile --
+// A tile that several parameters, dead slots or a row gap share.  The block copies the places,
+// scalars and rows of its parameters into LDS in one round of loads, kTileParams of them at a
+// time, so that a column's owner costs no chain of global loads.  A tile of more parameters is
+// gone through once per kTileParams: a column is taken when its owner is there.
+constexpr int kTileParams = 256;
+struct TileMap {
+    float4 scal[kTileParams];
+    int64_t row[kTileParams];   // arena index of the tile's first column in the parameter's own row
+    int32_t begin[kTileParams], end[kTileParams];  // columns relative to the tile, cut to it
+    int count;
+
+    __device__ __forceinline__ int find(int xr) const {  // first k whose range ends after xr
+        int lo = 0, hi = count;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (end[mid] > xr) hi = mid; else lo = mid + 1;
+        }
+        return lo;
+    }
+    __device__ __forceinline__ bool holds(int k, int xr) const { return k < count && begin[k] <= xr; }
+    __device__ __forceinline__ AdamWScal scalars(int k) const { return scal_of(scal[k]); }
+};
+__device__ __forceinline__ int32_t cut_to_tile(int64_t x) { return int32_t(x < 0 ? 0 : x > kTileCols ? kTileCols : x); }
+
+// f(first) for every kTileParams parameters [first, ..) of mixed tile j with M filled, all threads
+// of the block in it, a barrier after each: what f reads of LDS may be written again.
+template <class F>
+__device__ __forceinline__ void mixed_tile(TileMap& M, const DevPlan& P, const float4* scal, const Tile& T, int64_t j,
+                                           F f) {
+    const int64_t last = ld_const(P.tile_first, j + 1);  // reaches past the tile, or does not exist
+    const int64_t end = last < P.n ? last + 1 : P.n;
+#pragma unroll 1
+    for (int64_t first = T.first; first < end; first += kTileParams) {
+        const int k = threadIdx.x;
+        const int64_t i = first + k;
+        if (i < end) {
+            M.begin[k] = cut_to_tile(P.off[i] - T.x0);
+            M.end[k] = cut_to_tile(P.end[i] - T.x0);
+            M.scal[k] = scal[i];
+            const int32_t b = P.bucket[i];
+            const int64_t O = P.b_base[b];
+            M.row[k] = P.nd * O + P.rank * P.b_stride[b] + (T.x0 - O);
+        }
+        if (k == 0) M.count = int(end - first < kTileParams ? end - first : kTileParams);
+        __syncthreads();
+        f(first);
+        __syncthreads();
+    }
+}
+static_assert(kTileParams == kBlock, "a thread per parameter of the map");
 
 // ------------------------------------------------------------------------- 32-bit states --
 // One element in fp32 with every rounding spelled out.  Without decay (shrink = 0) the bits are
@@ -57,6 +134,20 @@ template <int DT>
 __device__ __forceinline__ uint64_t pack4(const float4& p) {
     return uint64_t(uint32_t(from_f32<DT>(p.x)) | (uint32_t(from_f32<DT>(p.y)) << 16)) |
            uint64_t(uint32_t(from_f32<DT>(p.z)) | (uint32_t(from_f32<DT>(p.w)) << 16)) << 32;
+}
+// Four fp32 values rounded to 16 bits, to the nearest even.  bf16 has a conversion instruction for
+// pairs, which agrees with from_f32 on every value but the payload of a NaN.
+typedef float zs_pair_f32 __attribute__((ext_vector_type(2)));
+typedef __bf16 zs_pair_bf16 __attribute__((ext_vector_type(2)));
+template <int DT>
+__device__ __forceinline__ uint64_t pack4_fast(const float4& p) {
+    if constexpr (DT == ZERO_BF16) {
+        const zs_pair_f32 a = {p.x, p.y}, b = {p.z, p.w};
+        return uint64_t(__builtin_bit_cast(uint32_t, __builtin_convertvector(a, zs_pair_bf16))) |
+               uint64_t(__builtin_bit_cast(uint32_t, __builtin_convertvector(b, zs_pair_bf16))) << 32;
+    } else {
+        return pack4<DT>(p);
+    }
 }
 __device__ __forceinline__ void store8(uint16_t* to, uint64_t v) {
     __builtin_nontemporal_store(v, gptr(reinterpret_cast<uint64_t*>(to)));
@@ -75,6 +166,34 @@ __device__ __forceinline__ void adamw_quad(const AdamK& K, const AdamWScal& s, c
     store4f(mm, m);
     store4f(vv, v);
     store8(lp, pack4<DT>(p));
+}
+
+// The same for 4 columns of a mixed tile, xr the first's place in it: whole where they lie inside
+// one parameter, else column by column, only live ones written.  All of them were loaded before
+// their owners were known; what belongs to nobody is not used.
+template <int DT>
+__device__ __forceinline__ void adamw_quad_mixed(const TileMap& M, const AdamK& K, int xr, const float4& g, float4 p,
+                                                 float4 m, float4 v, float* p32, float* mm, float* vv, uint16_t* arena) {
+    int k = M.find(xr);
+    if (M.holds(k, xr) && M.end[k] >= xr + 4) {
+        const AdamWScal s = M.scalars(k);
+        if (s.live()) adamw_quad<DT>(K, s, g, p, m, v, p32, mm, vv, arena + M.row[k] + xr);
+        return;
+    }
+    const float* gq = &g.x;
+    float *pq = &p.x, *mq = &m.x, *vq = &v.x;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        while (k < M.count && M.end[k] <= xr + t) ++k;
+        if (!M.holds(k, xr + t)) continue;
+        const AdamWScal s = M.scalars(k);
+        if (!s.live()) continue;
+        adamw_elem(K, s, gq[t], pq[t], mq[t], vq[t]);
+        gptr(p32)[t] = pq[t];
+        gptr(mm)[t] = mq[t];
+        gptr(vv)[t] = vq[t];
+        gptr(arena)[M.row[k] + xr + t] = from_f32<DT>(pq[t]);
+    }
 }
 
 // -------------------------------------------------------------------------- 8-bit states --
@@ -115,7 +234,7 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
 
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 __device__ __forceinline__ float pow2_of_byte(uint32_t b) { return __uint_as_float(b << 23); }  // 255 -> +inf
-// 2^(127 - b); 0 for the not-finite block (its codes become 0)
+// 2^(127 - b); 0 for the block that is not finite (its codes become 0)
 __device__ __forceinline__ float inverse_of_byte(uint32_t b) { return __uint_as_float((b == kScaleNan ? 0u : 254u - b) << 23); }
 
 // Scale bytes from the bits of a block's largest magnitude (any NaN or infinity compares above
@@ -130,49 +249,74 @@ __device__ __forceinline__ uint32_t root_byte(uint32_t big) {
     return big >= 0x7f800000u ? kScaleNan : (e < 32u ? 32u : e);
 }
 
-// Codes.  Multiplying by the inverse scale is exact; the second factor moves the code's exponent
-// range onto fp32's smallest exponents, so that the code is the number's leading bits, its own
-// subnormals falling on fp32's.  `noise` is added below the code's last bit.
-__device__ __forceinline__ uint32_t moment_code(float m, float inverse, uint32_t noise) {
-    const uint32_t t = __float_as_uint((__uint_as_float(abs_bits(m)) * inverse) * 0x1p-120f);
-    return ((t + noise) >> 20) | ((__float_as_uint(m) >> 24) & 0x80u);
+// Decoding.  The momentum's code has a conversion instruction.  The root's becomes the leading bits
+// of an fp32 number with the smallest exponents (its subnormals fall on fp32's), moved in place by
+// ldexp: code << 19 stands for its value times 2^-112.
+typedef float zs_f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void moment_values(uint32_t word, float (&m)[4]) {
+    const zs_f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(word), false);
+    const zs_f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(int(word), true);
+    m[0] = a.x;
+    m[1] = a.y;
+    m[2] = b.x;
+    m[3] = b.y;
 }
-__device__ __forceinline__ uint32_t root_code(float r, float inverse, uint32_t noise) {
-    const uint32_t t = __float_as_uint((r * inverse) * 0x1p-112f);
-    const uint32_t c = (t + noise) >> 19;
+__device__ __forceinline__ float root_value(uint32_t code, uint32_t byte) {
+    const float r = __builtin_amdgcn_ldexpf(__uint_as_float(code << 19), int(byte) - 15);
+    return byte == kScaleNan ? __builtin_nanf("") : r;
+}
+
+// Rounding codes of scaled values.  The momentum's instruction adds the noise's 20 high bits below
+// the code's last bit; for the root they are added by hand.
+template <int SEL>
+__device__ __forceinline__ uint32_t moment_round(float scaled, uint32_t noise, uint32_t word) {
+    return uint32_t(__builtin_amdgcn_cvt_sr_fp8_f32(scaled, noise, int(word), SEL));
+}
+__device__ __forceinline__ uint32_t root_bits(float r, uint32_t byte) {
+    return __float_as_uint(__builtin_amdgcn_ldexpf(r, 15 - int(byte)));
+}
+__device__ __forceinline__ uint32_t root_round(float r, uint32_t byte, uint32_t noise) {
+    const uint32_t c = (root_bits(r, byte) + noise) >> 19;
     return c == 0u && r > 0.0f ? 1u : c;
 }
 // To the nearest, ties to the even code.
-__device__ __forceinline__ uint32_t moment_code_near(float m, float inverse) {
-    const uint32_t t = __float_as_uint((__uint_as_float(abs_bits(m)) * inverse) * 0x1p-120f);
-    return moment_code(m, inverse, 0x7ffffu + ((t >> 20) & 1u));
+__device__ __forceinline__ uint32_t moment_near(float m, uint32_t byte) {
+    const uint32_t t = __float_as_uint((__uint_as_float(abs_bits(m)) * inverse_of_byte(byte)) * 0x1p-120f);
+    return ((t + 0x7ffffu + ((t >> 20) & 1u)) >> 20) | ((__float_as_uint(m) >> 24) & 0x80u);
 }
-__device__ __forceinline__ uint32_t root_code_near(float r, float inverse) {
-    const uint32_t t = __float_as_uint((r * inverse) * 0x1p-112f);
-    return root_code(r, inverse, 0x3ffffu + ((t >> 19) & 1u));
+__device__ __forceinline__ uint32_t root_near(float r, uint32_t byte) {
+    return root_round(r, byte, 0x3ffffu + ((root_bits(r, byte) >> 19) & 1u));
 }
-__device__ __forceinline__ float moment_value(uint32_t code) {
-    return __uint_as_float(((code & 0x7fu) << 20) | ((code & 0x80u) << 24)) * 0x1p120f;
-}
-__device__ __forceinline__ float root_value(uint32_t code) { return __uint_as_float(code << 19) * 0x1p112f; }
 
 // The noise of column x for a parameter's key.
 __device__ __forceinline__ uint32_t noise_of(uint32_t key, int64_t x) {
     return mix32(uint32_t(x) ^ key ^ (uint32_t(uint64_t(x) >> 32) * kRoot3));
 }
-__device__ __forceinline__ uint32_t moment_noise(uint32_t h) { return ((h & 0xffffu) << 4) + 8u; }
-__device__ __forceinline__ uint32_t root_noise(uint32_t h) { return ((h >> 16) << 3) + 4u; }
+// 16 bits each and half of what is below them: for m at the top of 20 of 32 bits, for r as 19 bits
+__device__ __forceinline__ uint32_t moment_noise(uint32_t h) { return (h << 16) | 0x8000u; }
+__device__ __forceinline__ uint32_t root_noise(uint32_t h) { return ((h >> 13) & ~7u) | 4u; }
+
+// Square root to within a unit in the last place: the reciprocal root's estimate and one Newton
+// step with the exact residual, half the instructions of the correctly rounded sequence, from which
+// it differs once in 10^4 values.  0 gives 0; below 2^-126 it falls short.
+__device__ __forceinline__ float root_of(float v) {
+    const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));
+    const float q = v * y;
+    return __builtin_fmaf(__builtin_fmaf(-q, q, v), 0.5f * y, q);
+}
 
 // One element from the decoded states: new p, m and r, not yet rounded to 8 bits.  Products and
-// sums are rounded one by one, no contraction: a value next to a code's border then falls on the
-// side that the formula in fp32 gives.
+// sums of m and v are rounded one by one, no contraction: a value next to a code's border then
+// falls on the side that the formula in fp32 gives.  The quotient is m times the reciprocal's
+// estimate (a unit): with a division and a root correctly rounded the step's arithmetic takes as
+// long as its memory traffic, and both round the update, not the state.
 __device__ __forceinline__ void adamw8_elem(const AdamK& K, const AdamWScal& s, float g32, float& p, float& m, float& r) {
 #pragma clang fp contract(off)
     const float g = g32 * K.gs;
     m = K.b1 * m + K.c1 * g;
-    r = sqrtf(K.b2 * (r * r) + K.c2 * (g * g));
+    r = root_of(K.b2 * (r * r) + K.c2 * (g * g));
     p = __builtin_fmaf(-s.shrink, p, p);
-    p = __builtin_fmaf(-s.step, m / __builtin_fmaf(r, s.inv_sqrt_bc2, K.eps), p);
+    p = __builtin_fmaf(-s.step, m * __builtin_amdgcn_rcpf(__builtin_fmaf(r, s.inv_sqrt_bc2, K.eps)), p);
 }
 
 // Largest of a value over the 64 lanes (every lane active), in a scalar register: shifts within
@@ -192,9 +336,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
 }
 __device__ __forceinline__ uint32_t max4_bits(float a, float b, float c, float d) {
-    const uint32_t x = abs_bits(a) > abs_bits(b) ? abs_bits(a) : abs_bits(b);
-    const uint32_t y = abs_bits(c) > abs_bits(d) ? abs_bits(c) : abs_bits(d);
-    return x > y ? x : y;
+    return max(max(max(abs_bits(a), abs_bits(b)), abs_bits(c)), abs_bits(d));
 }
 
 // What an 8-bit step works on.
@@ -203,7 +345,6 @@ struct AdamW8Args {
     uint8_t* m8;
     uint8_t* r8;
     uint16_t* scales;  // [n_scales] low byte m's, high byte r's
-    const uint8_t* live;
     const float4* scal;
     const float* consts;
     const int32_t* flag;
@@ -215,24 +356,27 @@ struct Run8 {
     float4 p;
     uint32_t m8, r8, scale;
 };
-__device__ __forceinline__ Run8 run8_load(const AdamW8Args& A, int64_t x, int64_t block) {
+__device__ __forceinline__ Run8 run8_load(const AdamW8Args& A, int64_t x) {
     Run8 q;
     q.p = load4f_nt(A.p32 + x);
     q.m8 = __builtin_nontemporal_load(gptr(reinterpret_cast<const uint32_t*>(A.m8 + x)));
     q.r8 = __builtin_nontemporal_load(gptr(reinterpret_cast<const uint32_t*>(A.r8 + x)));
-    q.scale = gptr(A.scales)[block];
+    q.scale = 0;
     return q;
 }
-template <int DT>
-__device__ __forceinline__ void run8_step(const AdamK& K, const AdamWScal& s, const AdamW8Args& A, int64_t x,
-                                          int64_t block, const float4& g, Run8 q, uint16_t* lp) {
+struct Out8 {
+    uint32_t m8, r8, scale;
+};
+// New states of the run, q.p updated in place.
+__device__ __forceinline__ Out8 run8_math(const AdamK& K, const AdamWScal& s, int64_t x, const float4& g, Run8& q) {
     const uint32_t pair = uint32_t(__builtin_amdgcn_readfirstlane(int(q.scale)));
-    const float ms = pow2_of_byte(pair & 0xffu), rs = pow2_of_byte(pair >> 8);
+    const float ms = pow2_of_byte(pair & 0xffu);
     float m[4], r[4];
+    moment_values(q.m8, m);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        m[t] = moment_value((q.m8 >> (8 * t)) & 0xffu) * ms;
-        r[t] = root_value((q.r8 >> (8 * t)) & 0xffu) * rs;
+        m[t] *= ms;
+        r[t] = root_value((q.r8 >> (8 * t)) & 0xffu, pair >> 8);
     }
     adamw8_elem(K, s, g.x, q.p.x, m[0], r[0]);
     adamw8_elem(K, s, g.y, q.p.y, m[1], r[1]);
@@ -240,21 +384,36 @@ __device__ __forceinline__ void run8_step(const AdamK& K, const AdamWScal& s, co
     adamw8_elem(K, s, g.w, q.p.w, m[3], r[3]);
     const uint32_t mb = moment_byte(wave_max(max4_bits(m[0], m[1], m[2], m[3])));
     const uint32_t rb = root_byte(wave_max(max4_bits(r[0], r[1], r[2], r[3])));
-    const float mi = inverse_of_byte(mb), ri = inverse_of_byte(rb);
-    uint32_t mw = 0, rw = 0;
+    const float mi = inverse_of_byte(mb);
+    uint32_t h[4];
+    Out8 o{0, 0, mb | (rb << 8)};
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        const uint32_t h = noise_of(s.key, x + t);
-        mw |= moment_code(m[t], mi, moment_noise(h)) << (8 * t);
-        rw |= root_code(r[t], ri, root_noise(h)) << (8 * t);
+        h[t] = noise_of(s.key, x + t);
+        o.r8 |= root_round(r[t], rb, root_noise(h[t])) << (8 * t);
     }
-    if (mb == kScaleNan) mw = 0;
-    if (rb == kScaleNan) rw = 0;
-    store4f(A.p32 + x, q.p);
-    __builtin_nontemporal_store(mw, gptr(reinterpret_cast<uint32_t*>(A.m8 + x)));
-    __builtin_nontemporal_store(rw, gptr(reinterpret_cast<uint32_t*>(A.r8 + x)));
-    store8(lp, pack4<DT>(q.p));
-    if (__lane_id() == 0) gptr(A.scales)[block] = uint16_t(mb | (rb << 8));
+    o.m8 = moment_round<0>(m[0] * mi, moment_noise(h[0]), o.m8);
+    o.m8 = moment_round<1>(m[1] * mi, moment_noise(h[1]), o.m8);
+    o.m8 = moment_round<2>(m[2] * mi, moment_noise(h[2]), o.m8);
+    o.m8 = moment_round<3>(m[3] * mi, moment_noise(h[3]), o.m8);
+    if (mb == kScaleNan) o.m8 = 0;
+    if (rb == kScaleNan) o.r8 = 0;
+    return o;
+}
+template <int DT>
+__device__ __forceinline__ void run8_store(const AdamW8Args& A, int64_t x, int64_t block, const float4& p, const Out8& o,
+                                           uint16_t* lp) {
+    store4f(A.p32 + x, p);
+    __builtin_nontemporal_store(o.m8, gptr(reinterpret_cast<uint32_t*>(A.m8 + x)));
+    __builtin_nontemporal_store(o.r8, gptr(reinterpret_cast<uint32_t*>(A.r8 + x)));
+    store8(lp, pack4_fast<DT>(p));
+    if (__lane_id() == 0) gptr(A.scales)[block] = uint16_t(o.scale);
+}
+template <int DT>
+__device__ __forceinline__ void run8_step(const AdamK& K, const AdamWScal& s, const AdamW8Args& A, int64_t x,
+                                          int64_t block, const float4& g, Run8 q, uint16_t* lp) {
+    const Out8 o = run8_math(K, s, x, g, q);
+    run8_store<DT>(A, x, block, q.p, o, lp);
 }
 
 // A wavefront's scratch for a run of several blocks: the largest magnitudes of m and r of every
@@ -269,56 +428,75 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// The blocks of a run that holds several parameters, dead slots or a row gap: the columns
-// [lo, hi) of it that belong to live parameters, element by element.  x: the lane's first column;
-// i: the first parameter whose range ends after x; g_of(x): the reduced gradient of a column.
-template <int DT, class G>
-__device__ __forceinline__ void run8_mixed(const DevPlan& P, const AdamK& K, const AdamW8Args& A, RunMax* S, int64_t x,
-                                           int64_t i, int64_t lo, int64_t hi, G g_of) {
-    const int64_t run = x & ~(kRun - 1);
-    const uint32_t l4 = uint32_t(x - run);
-    float m[4] = {0, 0, 0, 0}, r[4] = {0, 0, 0, 0};
-    int64_t own[4];
-    uint32_t first[4];
+// The lane's 4 columns of a run of a mixed tile, xr the first's place in it, x in the shard; every
+// lane of the wavefront calls it (`in`: whether its columns exist; q.scale is not used).  A run
+// that one parameter covers is the step above.  Else the blocks' largest magnitudes go through
+// the wavefront's scratch, and only live columns are written.
+template <int DT>
+__device__ __forceinline__ void run8_mixed(const TileMap& M, const AdamK& K, const AdamW8Args& A, RunMax* S, int64_t first,
+                                           int64_t x, int xr, bool in, const float4& g, Run8 q) {
+    const int run = xr & ~int(kRun - 1), l4 = xr - run;
+    const int64_t block = (x >> kRunShift) + first;
+    int k = M.find(xr);
+    if (M.holds(k, run) && M.end[k] >= run + kRun) {  // the same k in every lane
+        const AdamWScal s = M.scalars(k);
+        if (!s.live()) return;
+        q.scale = gptr(A.scales)[block + k];
+        run8_step<DT>(K, s, A, x, block + k, g, q, A.arena + M.row[k] + xr);
+        return;
+    }
+    const float* gq = &g.x;
+    float* pq = &q.p.x;
+    int own[4], at[4];
+    uint32_t pair[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         S->m[l4 + t] = 0;
         S->r[l4 + t] = 0;
+        while (k < M.count && M.end[k] <= xr + t) ++k;
+        const bool on = in && M.holds(k, xr + t) && M.scalars(k).live();
+        own[t] = on ? k : -1;
+        at[t] = on && M.begin[k] > run ? M.begin[k] - run : 0;
+        pair[t] = on ? gptr(A.scales)[block + k] : 0;
     }
     wave_lds_fence();
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int64_t xt = x + t;
-        own[t] = -1;
-        first[t] = 0;
-        if (xt < lo || xt >= hi) continue;
-        while (i < P.n && P.end[i] <= xt) ++i;
-        if (!(i < P.n && P.off[i] <= xt) || !A.live[i]) continue;
-        own[t] = i;
-        first[t] = uint32_t((P.off[i] > run ? P.off[i] : run) - run);
-        const uint32_t pair = gptr(A.scales)[(run >> kRunShift) + i];
-        const AdamWScal s = scal_of(A.scal[i]);
-        float p = gptr(A.p32)[xt];
-        m[t] = moment_value(gptr(A.m8)[xt]) * pow2_of_byte(pair & 0xffu);
-        r[t] = root_value(gptr(A.r8)[xt]) * pow2_of_byte(pair >> 8);
-        adamw8_elem(K, s, g_of(xt), p, m[t], r[t]);
-        gptr(A.p32)[xt] = p;
-        const int32_t b = P.bucket[i];
-        const int64_t O = P.b_base[b];
-        gptr(A.arena)[P.nd * O + P.rank * P.b_stride[b] + (xt - O)] = from_f32<DT>(p);
-        atomicMax(&S->m[first[t]], abs_bits(m[t]));
-        atomicMax(&S->r[first[t]], abs_bits(r[t]));
-    }
-    wave_lds_fence();  // also: every lane has read its old scales before one is written
+    float m[4], r[4];
+    moment_values(q.m8, m);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         if (own[t] < 0) continue;
-        const int64_t xt = x + t;
-        const uint32_t mb = moment_byte(S->m[first[t]]), rb = root_byte(S->r[first[t]]);
-        const uint32_t h = noise_of(scal_of(A.scal[own[t]]).key, xt);
-        gptr(A.m8)[xt] = mb == kScaleNan ? 0 : uint8_t(moment_code(m[t], inverse_of_byte(mb), moment_noise(h)));
-        gptr(A.r8)[xt] = rb == kScaleNan ? 0 : uint8_t(root_code(r[t], inverse_of_byte(rb), root_noise(h)));
-        if (l4 + t == first[t]) gptr(A.scales)[(run >> kRunShift) + own[t]] = uint16_t(mb | (rb << 8));
+        m[t] *= pow2_of_byte(pair[t] & 0xffu);
+        r[t] = root_value((q.r8 >> (8 * t)) & 0xffu, pair[t] >> 8);
+        adamw8_elem(K, M.scalars(own[t]), gq[t], pq[t], m[t], r[t]);
+        atomicMax(&S->m[at[t]], abs_bits(m[t]));
+        atomicMax(&S->r[at[t]], abs_bits(r[t]));
+    }
+    wave_lds_fence();  // also: every lane has its old scales before one is written
+    uint32_t mw = 0, rw = 0;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        if (own[t] < 0) continue;
+        const uint32_t mb = moment_byte(S->m[at[t]]), rb = root_byte(S->r[at[t]]);
+        const uint32_t h = noise_of(M.scalars(own[t]).key, x + t);
+        if (mb != kScaleNan)
+            mw |= (moment_round<0>(m[t] * inverse_of_byte(mb), moment_noise(h), 0) & 0xffu) << (8 * t);
+        if (rb != kScaleNan) rw |= root_round(r[t], rb, root_noise(h)) << (8 * t);
+        if (l4 + t == at[t]) gptr(A.scales)[block + own[t]] = uint16_t(mb | (rb << 8));
+    }
+    if (own[0] >= 0 && own[0] == own[3]) {
+        store4f(A.p32 + x, q.p);
+        *gptr(reinterpret_cast<uint32_t*>(A.m8 + x)) = mw;
+        *gptr(reinterpret_cast<uint32_t*>(A.r8 + x)) = rw;
+        store8(A.arena + M.row[own[0]] + xr, pack4<DT>(q.p));
+    } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (own[t] < 0) continue;
+            gptr(A.p32)[x + t] = pq[t];
+            gptr(A.m8)[x + t] = uint8_t(mw >> (8 * t));
+            gptr(A.r8)[x + t] = uint8_t(rw >> (8 * t));
+            gptr(A.arena)[M.row[own[t]] + xr + t] = from_f32<DT>(pq[t]);
+        }
     }
     wave_lds_fence();  // the scratch is free for the wavefront's next run
 }
