@@ -144,6 +144,7 @@ __global__ __launch_bounds__(kBlock) void adamw8_unload_kernel(DevPlan P, const 
                                                                const uint8_t* __restrict__ r8,
                                                                const uint16_t* __restrict__ scales,
                                                                uint16_t* __restrict__ m16, uint16_t* __restrict__ r16) {
+    __shared__ TilePlaces places;
     for (int64_t j = blockIdx.x; j < P.n_tiles; j += gridDim.x) {
         const int64_t x0 = j << kTileShift;
         const int64_t x = x0 + int64_t(threadIdx.x) * kChunk;
@@ -153,23 +154,28 @@ __global__ __launch_bounds__(kBlock) void adamw8_unload_kernel(DevPlan P, const 
             unload8(m8 + x, r8 + x, gptr(scales)[(x >> kRunShift) + ic], m16 + x, r16 + x);
             continue;
         }
-        if (x >= P.shard_numel) continue;
-        int64_t i = param_of_column(P, x);
-        if (i < P.n && P.off[i] <= x && x + kChunk <= P.end[i]) {
-            unload8(m8 + x, r8 + x, gptr(scales)[(x >> kRunShift) + i], m16 + x, r16 + x);
-            continue;
-        }
+        for_places(
+            places, P, j, iu, [](int, int64_t) {},
+            [&](int64_t first) {
+                if (x >= P.shard_numel) return;
+                const int xr = int(x - x0);
+                const int64_t block = (x >> kRunShift) + first;
+                int k = places.find(xr);
+                if (places.holds(k, xr) && places.end[k] >= xr + kChunk) {
+                    unload8(m8 + x, r8 + x, gptr(scales)[block + k], m16 + x, r16 + x);
+                    return;
+                }
 #pragma unroll
-        for (int t = 0; t < kChunk; ++t) {
-            const int64_t xt = x + t;
-            while (i < P.n && P.end[i] <= xt) ++i;
-            if (!(i < P.n && P.off[i] <= xt)) continue;
-            const uint32_t pair = gptr(scales)[(x >> kRunShift) + i];
-            float m[4];
-            moment_values(gptr(m8)[xt], m);
-            gptr(m16)[xt] = uint16_t(bf16_pair(m[0] * pow2_of_byte(pair & 0xffu), 0.0f));
-            gptr(r16)[xt] = uint16_t(bf16_pair(root_value(gptr(r8)[xt], pair >> 8), 0.0f));
-        }
+                for (int t = 0; t < kChunk; ++t) {
+                    while (k < places.count && places.end[k] <= xr + t) ++k;
+                    if (!places.holds(k, xr + t)) continue;
+                    const uint32_t pair = gptr(scales)[block + k];
+                    float m[4];
+                    moment_values(gptr(m8)[x + t], m);
+                    gptr(m16)[x + t] = uint16_t(bf16_pair(m[0] * pow2_of_byte(pair & 0xffu), 0.0f));
+                    gptr(r16)[x + t] = uint16_t(bf16_pair(root_value(gptr(r8)[x + t], pair >> 8), 0.0f));
+                }
+            });
     }
 }
 

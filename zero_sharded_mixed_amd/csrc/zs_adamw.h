@@ -76,9 +76,7 @@ struct Tile {
 // time, so that a column's owner costs no chain of global loads.  A tile of more parameters is
 // gone through once per kTileParams: a column is taken when its owner is there.
 constexpr int kTileParams = 256;
-struct TileMap {
-    float4 scal[kTileParams];
-    int64_t row[kTileParams];   // arena index of the tile's first column in the parameter's own row
+struct TilePlaces {
     int32_t begin[kTileParams], end[kTileParams];  // columns relative to the tile, cut to it
     int count;
 
@@ -91,36 +89,51 @@ struct TileMap {
         return lo;
     }
     __device__ __forceinline__ bool holds(int k, int xr) const { return k < count && begin[k] <= xr; }
+};
+struct TileMap : TilePlaces {
+    float4 scal[kTileParams];
+    int64_t row[kTileParams];  // arena index of the tile's first column in the parameter's own row
     __device__ __forceinline__ AdamWScal scalars(int k) const { return scal_of(scal[k]); }
 };
 __device__ __forceinline__ int32_t cut_to_tile(int64_t x) { return int32_t(x < 0 ? 0 : x > kTileCols ? kTileCols : x); }
 
-// f(first) for every kTileParams parameters [first, ..) of mixed tile j with M filled, all threads
-// of the block in it, a barrier after each: what f reads of LDS may be written again.
-template <class F>
-__device__ __forceinline__ void mixed_tile(TileMap& M, const DevPlan& P, const float4* scal, const Tile& T, int64_t j,
-                                           F f) {
+// For every kTileParams parameters [first, ..) of mixed tile j, `from` the first of them all: M filled
+// (and more(k, i) for entry k, parameter i), then f(first), all threads of the block in it, and a
+// barrier: what f reads of LDS may be written again.
+template <class M, class More, class F>
+__device__ __forceinline__ void for_places(M& map, const DevPlan& P, int64_t j, int64_t from, More more, F f) {
+    const int64_t x0 = j << kTileShift;
     const int64_t last = ld_const(P.tile_first, j + 1);  // reaches past the tile, or does not exist
     const int64_t end = last < P.n ? last + 1 : P.n;
 #pragma unroll 1
-    for (int64_t first = T.first; first < end; first += kTileParams) {
+    for (int64_t first = from; first < end; first += kTileParams) {
         const int k = threadIdx.x;
         const int64_t i = first + k;
         if (i < end) {
-            M.begin[k] = cut_to_tile(P.off[i] - T.x0);
-            M.end[k] = cut_to_tile(P.end[i] - T.x0);
-            M.scal[k] = scal[i];
-            const int32_t b = P.bucket[i];
-            const int64_t O = P.b_base[b];
-            M.row[k] = P.nd * O + P.rank * P.b_stride[b] + (T.x0 - O);
+            map.begin[k] = cut_to_tile(P.off[i] - x0);
+            map.end[k] = cut_to_tile(P.end[i] - x0);
+            more(k, i);
         }
-        if (k == 0) M.count = int(end - first < kTileParams ? end - first : kTileParams);
+        if (k == 0) map.count = int(end - first < kTileParams ? end - first : kTileParams);
         __syncthreads();
         f(first);
         __syncthreads();
     }
 }
 static_assert(kTileParams == kBlock, "a thread per parameter of the map");
+template <class F>
+__device__ __forceinline__ void mixed_tile(TileMap& M, const DevPlan& P, const float4* scal, const Tile& T, int64_t j,
+                                           F f) {
+    for_places(
+        M, P, j, T.first,
+        [&](int k, int64_t i) {
+            M.scal[k] = scal[i];
+            const int32_t b = P.bucket[i];
+            const int64_t O = P.b_base[b];
+            M.row[k] = P.nd * O + P.rank * P.b_stride[b] + (T.x0 - O);
+        },
+        f);
+}
 
 // ------------------------------------------------------------------------- 32-bit states --
 // One element in fp32 with every rounding spelled out.  Without decay (shrink = 0) the bits are
@@ -168,31 +181,48 @@ __device__ __forceinline__ void adamw_quad(const AdamK& K, const AdamWScal& s, c
     store8(lp, pack4<DT>(p));
 }
 
-// The same for 4 columns of a mixed tile, xr the first's place in it: whole where they lie inside
-// one parameter, else column by column, only live ones written.  All of them were loaded before
-// their owners were known; what belongs to nobody is not used.
+// The same for 4 columns of a mixed tile, xr the first's place in it; columns of dead parameters or of
+// nobody are loaded and not written.  Where every lane's columns lie inside one parameter each, as
+// above; else each column is computed with its owner's scalars in all lanes alike (one lane's
+// boundary would otherwise cost the wavefront both ways).
 template <int DT>
 __device__ __forceinline__ void adamw_quad_mixed(const TileMap& M, const AdamK& K, int xr, const float4& g, float4 p,
                                                  float4 m, float4 v, float* p32, float* mm, float* vv, uint16_t* arena) {
+    const float* gq = &g.x;
+    float *pq = &p.x, *mq = &m.x, *vq = &v.x;
     int k = M.find(xr);
-    if (M.holds(k, xr) && M.end[k] >= xr + 4) {
+    const bool one = M.holds(k, xr) && M.end[k] >= xr + 4;
+    if (__all(one)) {
         const AdamWScal s = M.scalars(k);
         if (s.live()) adamw_quad<DT>(K, s, g, p, m, v, p32, mm, vv, arena + M.row[k] + xr);
         return;
     }
-    const float* gq = &g.x;
-    float *pq = &p.x, *mq = &m.x, *vq = &v.x;
+    int64_t row[4];  // -1: not written
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         while (k < M.count && M.end[k] <= xr + t) ++k;
+        row[t] = -1;
         if (!M.holds(k, xr + t)) continue;
         const AdamWScal s = M.scalars(k);
         if (!s.live()) continue;
+        row[t] = M.row[k];
         adamw_elem(K, s, gq[t], pq[t], mq[t], vq[t]);
+    }
+    // rows of one bucket are one
+    if (row[0] >= 0 && row[0] == row[1] && row[0] == row[2] && row[0] == row[3]) {
+        store4f(p32, p);
+        store4f(mm, m);
+        store4f(vv, v);
+        store8(arena + row[0] + xr, pack4<DT>(p));
+        return;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        if (row[t] < 0) continue;
         gptr(p32)[t] = pq[t];
         gptr(mm)[t] = mq[t];
         gptr(vv)[t] = vq[t];
-        gptr(arena)[M.row[k] + xr + t] = from_f32<DT>(pq[t]);
+        gptr(arena)[row[t] + xr + t] = from_f32<DT>(pq[t]);
     }
 }
 
@@ -483,7 +513,8 @@ __device__ __forceinline__ void run8_mixed(const TileMap& M, const AdamK& K, con
         if (rb != kScaleNan) rw |= root_round(r[t], rb, root_noise(h)) << (8 * t);
         if (l4 + t == at[t]) gptr(A.scales)[block + own[t]] = uint16_t(mb | (rb << 8));
     }
-    if (own[0] >= 0 && own[0] == own[3]) {
+    const bool all = own[0] >= 0 && own[1] >= 0 && own[2] >= 0 && own[3] >= 0;
+    if (all && M.row[own[0]] == M.row[own[3]]) {  // rows of one bucket are one
         store4f(A.p32 + x, q.p);
         *gptr(reinterpret_cast<uint32_t*>(A.m8 + x)) = mw;
         *gptr(reinterpret_cast<uint32_t*>(A.r8 + x)) = rw;
