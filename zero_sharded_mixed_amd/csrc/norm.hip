@@ -1,7 +1,8 @@
 // norm.hip — the sum of squares of the reduced gradient over the live part of the shard, for
 // clipping by the global norm (the ranks add their sums; the step forms the coefficient).
 //
-// One read of the shard (4 bytes per element), bound by memory.  Squares and sums are in double:
+// One read of the shard (4 bytes per element), bound by memory: 120 us for the GPT-2 list's 194.7M
+// elements at Nd = 8 on MI355X (6.5 TB/s), and 5 us for adding the parts.  Squares and sums are in double:
 // the square of any fp32 value is exact there and cannot overflow, so the sum is finite exactly
 // when every live value is, which makes the overflow verdict free.  The shard's tiles are dealt
 // to at most kNormParts parts, each summed by one block in a fixed order, and the parts are
@@ -11,8 +12,10 @@
 namespace zs {
 
 constexpr int kFinishBlock = 1024;  // threads of the block that adds the parts
-// Shards of at most this many tiles are summed by one block in one launch.
-constexpr int64_t kOneBlockTiles = 32;
+// Shards of at most this many tiles (of 2048 columns) are summed by one block in one launch.
+// Measured on MI355X, a call among others, one launch against two: 6.1 us against 9.5 at 4 tiles,
+// 6.6 against 9.5 at 15, 10.9 against 9.5 at 32 (4.9, 6.4 and 10.7 against 6.8 in a graph).
+constexpr int64_t kOneBlockTiles = 16;
 
 // Sum over the block's WAVES wavefronts, in thread 0: lanes by halving distance, then the
 // wavefronts in order.
