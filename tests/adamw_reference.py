@@ -79,7 +79,8 @@ def noise(seed: int, rank: int, t: np.ndarray, x: np.ndarray) -> np.ndarray:
     k = mix32(k ^ np.uint64(seed >> 32))
     key = mix32(np.asarray(t, np.uint64) ^ k)
     x = np.asarray(x, np.uint64)
-    return mix32((x & np.uint64(0xFFFFFFFF)) ^ key ^ (((x >> np.uint64(32)) * np.uint64(0xBB67AE85)) & np.uint64(0xFFFFFFFF)))
+    high = ((x >> np.uint64(32)) * np.uint64(0xBB67AE85)) & np.uint64(0xFFFFFFFF)
+    return mix32((x & np.uint64(0xFFFFFFFF)) ^ key ^ high)
 
 
 def encode(x, idx, on, n_scales, kind, h=None):

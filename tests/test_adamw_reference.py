@@ -36,7 +36,8 @@ def test_nearest_moment_codes_are_torch_s():
 
 @pytest.mark.parametrize("big,top,emax,least,want", [
     (448.0, 448.0, 8, -111, 0), (448.0001, 448.0, 8, -111, 1), (449.0, 448.0, 8, -111, 1), (256.0, 448.0, 8, -111, 0),
-    (255.9, 448.0, 8, -111, 0), (224.0, 448.0, 8, -111, -1), (1.9375, 1.9375, 0, -95, 0), (1.94, 1.9375, 0, -95, 1), (1e-38, 448.0, 8, -111, -111)])
+    (255.9, 448.0, 8, -111, 0), (224.0, 448.0, 8, -111, -1), (1.9375, 1.9375, 0, -95, 0),
+    (1.94, 1.9375, 0, -95, 1), (1e-38, 448.0, 8, -111, -111)])
 def test_scales(big, top, emax, least, want):
     """The least power of two under which the largest value does not pass the top code."""
     byte = R.block_bytes(np.array([big, -big / 3]), np.zeros(2, int), np.ones(2, bool), 1, top, emax, least)

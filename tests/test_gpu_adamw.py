@@ -29,6 +29,7 @@ def lists():
         "ragged-1": (ragged_numels(rng, 300, 1, 9000), 1, 0, 30000),
         "ragged-7": (ragged_numels(rng, 400, 7, 60000), 7, 5, 50000),
         "ragged-64": (ragged_numels(rng, 500, 64, 300000), 64, 63, 0),
+        "ragged-32": (ragged_numels(rng, 300, 32, 200000), 32, 9, 200000),
         "tiny": ([1] * 700 + [0] * 300 + [2] * 300 + [5000], 1, 0, 1000),
     }
 
@@ -603,6 +604,36 @@ def test_two_steps_of_one_plan_at_once():
     for a, b in zip(alone, both):
         for k in ("p32", "m8", "r8", "scales", "steps", "arena", "sumsq"):
             assert torch.equal(a[k], b[k]), k
+
+
+def test_a_shard_of_many_tiles():
+    """13,000 tiles: more than the sum has parts, and the size from which the 32-bit step limits its
+    blocks per CU; checked at 200,000 columns and against the sum of the squares in double."""
+    n0, n1 = 13000 * 2048 + 777, 5003
+    plan = Z.zero_plan_create([n0, n1], 1, 0, 0, Z.ZERO_BF16)
+    S = plan.shard_numel
+    say(f"[many tiles] {S} columns")
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(19)
+    rnd = lambda k: torch.randn(S, generator=gen, device=DEV) * k  # noqa: E731
+    g, p, m, v = rnd(1e-2), rnd(2e-2), rnd(3e-3), rnd(1e-2).square()
+    old = [x.clone() for x in (p, m, v)]
+    live, steps = torch.ones(2, dtype=torch.uint8, device=DEV), torch.full((2,), 41, dtype=torch.int32, device=DEV)
+    work = torch.zeros(plan.adamw_work_bytes, dtype=torch.uint8, device=DEV)
+    arena, sumsq = torch.zeros(S, dtype=torch.bfloat16, device=DEV), torch.zeros(1, dtype=torch.float64, device=DEV)
+    Z.zero_grad_sumsq(plan, g, live, sumsq, work)
+    inside = (g[:n0 + n1].double() ** 2).sum().item()
+    assert abs(float(sumsq) / inside - 1) <= 2.0 ** -53 * S
+    hp = Z.AdamWParams(lr=1e-3, beta2=0.95, weight_decay=0.1, max_norm=0.5, grad_sumsq=sumsq)
+    Z.zero_adamw_step(plan, g, p, m, v, live, steps, hp, None, arena, work)
+    cols = np.unique(np.random.default_rng(20).integers(0, n0 + n1, 200000))
+    at = torch.from_numpy(cols).to(DEV)
+    pick = lambda t: host(t[at]).astype(np.float64)  # noqa: E731
+    ref = R.Step(dict(lr=1e-3, beta2=0.95, weight_decay=0.1, max_norm=0.5, sumsq=float(sumsq)), np.array([42, 42]), 2)
+    want, far = R.adamw64(ref, (cols >= n0).astype(np.int64), host(g[at]), *[pick(x) for x in old])
+    for name, got, w, e in zip("pmv", (p, m, v), want, far):
+        close(host(got[at]), w, e, np.ones(cols.size, bool), name)
+    assert torch.equal(arena[:n0 + n1], p[:n0 + n1].bfloat16())
 
 
 @pytest.mark.timeout(300)

@@ -7,19 +7,22 @@
 
 namespace zs {
 
-// Row forms (zs_common.h) and blocks per CU, by the number of rows and the states' bits, measured on
-// MI355X as the time of a step's launches: the GPT-2 list at Nd = 8, the 7.5B list at Nd = 64 and the
-// ragged list at Nd = 1024.
-//   32 bits, Nd >= kManyRows: fewest registers on whole tiles, two groups of rows in flight on the
-//     others (180 registers, two waves per SIMD): 3.28 ms and 0.82 ms; with one group on the others
-//     (five waves) 3.45 and 0.85;
-//   32 bits below: one group on the others, at four blocks per CU: 1.36 ms; 1.40 at five, 1.75 with
-//     two groups;
-//   8 bits, Nd >= kManyRows: the same, at three blocks per CU: 3.05 ms and 0.83 ms; 3.15 and 0.83 at
-//     five, 3.17 and 0.80 with two groups;
-//   8 bits below: a group of rows at once on whole tiles too, five blocks: 1.02 ms; 1.07 with fewest
-//     registers, 1.23 at three blocks.
-constexpr int64_t kManyRows = 16;
+// Row forms (zs_common.h) and blocks per CU go by the number of rows, with a border for each width
+// of the states.  Measured on MI355X, a step's launches on the GPT-2 list, the form for few rows
+// against the one for many:
+//   32 bits: 1.36 ms against 1.76 at Nd = 8, 1.00 against 1.12 at 16, 0.817 against 0.826 at 32, 0.723
+//     against 0.711 at 64;
+//   8 bits: 1.03 against 1.24 at 8, 0.83 against 0.88 at 16, 0.75 against 0.72 at 32, 0.69 against 0.66
+//     at 64.
+// Few rows, 32 bits: fewest registers on whole tiles, one group of rows in flight on the others, at
+//   four blocks per CU (1.40 ms at five at Nd = 8).
+// Many rows, 32 bits: two groups on the others (180 registers, two wavefronts per SIMD): 0.82 ms
+//   against 0.85 with one group on the ragged list at Nd = 1024.
+// Few rows, 8 bits: a group at once on whole tiles too, five blocks (1.07 ms with fewest registers,
+//   1.23 at three blocks).
+// Many rows, 8 bits: fewest registers, one group on the others, at three blocks (7.5B list, Nd = 64: 3.05
+//   ms; 3.15 at five, 3.17 with two groups).
+constexpr int64_t kManyRows = 48, kManyRows8 = 24;
 // Reserved where fewer blocks are faster: with the kernels' own 16 and 24 KB, four and three blocks
 // fit a CU's 160 KB.
 constexpr unsigned kFewBlocksLds = 16 * 1024;
@@ -191,12 +194,13 @@ extern "C" zero_status zero_reduce_adamw_bucket(const zero_plan* plan, int64_t b
     if ((st = check_work(d_work, who)) != ZERO_OK) return st;
     const int g = grid_for(B.n_tile);
     hipStream_t s = (hipStream_t)stream;
-    const bool big = plan->nd >= kManyRows;
-    auto kern = plan->dtype == ZERO_BF16
-                    ? (big ? reduce_adamw_kernel<ZERO_BF16, kRowsLow, kRowsPipe> : reduce_adamw_kernel<ZERO_BF16, kRowsLow, kRowsGroup>)
-                    : (big ? reduce_adamw_kernel<ZERO_FP16, kRowsLow, kRowsPipe> : reduce_adamw_kernel<ZERO_FP16, kRowsLow, kRowsGroup>);
-    kern<<<g, kBlock, big ? 0u : kFewBlocksLds, s>>>(plan->dev, B, d_live, d_p32, d_m, d_v, work_scal(d_work), work_consts(d_work), d_flag,
-                              static_cast<uint16_t*>(d_arena));
+    const bool bf16 = plan->dtype == ZERO_BF16, many = plan->nd >= kManyRows;
+    auto kern = many ? (bf16 ? reduce_adamw_kernel<ZERO_BF16, kRowsLow, kRowsPipe>
+                             : reduce_adamw_kernel<ZERO_FP16, kRowsLow, kRowsPipe>)
+                     : (bf16 ? reduce_adamw_kernel<ZERO_BF16, kRowsLow, kRowsGroup>
+                             : reduce_adamw_kernel<ZERO_FP16, kRowsLow, kRowsGroup>);
+    kern<<<g, kBlock, many ? 0u : kFewBlocksLds, s>>>(plan->dev, B, d_live, d_p32, d_m, d_v, work_scal(d_work),
+                                                      work_consts(d_work), d_flag, static_cast<uint16_t*>(d_arena));
     return check_launch(who);
 }
 
@@ -216,10 +220,11 @@ extern "C" zero_status zero_reduce_adamw8_bucket(const zero_plan* plan, int64_t 
     const AdamW8Args A{d_p32, d_m8, d_r8, reinterpret_cast<uint16_t*>(d_scales), work_scal(d_work),
                        work_consts(d_work), d_flag, static_cast<uint16_t*>(d_arena)};
     const int g = grid_for(B.n_tile);
-    const bool big = plan->nd >= kManyRows;
-    auto kern = plan->dtype == ZERO_BF16
-                    ? (big ? reduce_adamw8_kernel<ZERO_BF16, kRowsLow, kRowsGroup> : reduce_adamw8_kernel<ZERO_BF16, kRowsGroup, kRowsGroup>)
-                    : (big ? reduce_adamw8_kernel<ZERO_FP16, kRowsLow, kRowsGroup> : reduce_adamw8_kernel<ZERO_FP16, kRowsGroup, kRowsGroup>);
-    kern<<<g, kBlock, big ? kFewBlocksLds : 0u, (hipStream_t)stream>>>(plan->dev, B, d_live, A);
+    const bool bf16 = plan->dtype == ZERO_BF16, many = plan->nd >= kManyRows8;
+    auto kern = many ? (bf16 ? reduce_adamw8_kernel<ZERO_BF16, kRowsLow, kRowsGroup>
+                             : reduce_adamw8_kernel<ZERO_FP16, kRowsLow, kRowsGroup>)
+                     : (bf16 ? reduce_adamw8_kernel<ZERO_BF16, kRowsGroup, kRowsGroup>
+                             : reduce_adamw8_kernel<ZERO_FP16, kRowsGroup, kRowsGroup>);
+    kern<<<g, kBlock, many ? kFewBlocksLds : 0u, (hipStream_t)stream>>>(plan->dev, B, d_live, A);
     return check_launch(who);
 }

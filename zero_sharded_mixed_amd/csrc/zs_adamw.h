@@ -265,7 +265,9 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 __device__ __forceinline__ float pow2_of_byte(uint32_t b) { return __uint_as_float(b << 23); }  // 255 -> +inf
 // 2^(127 - b); 0 for the block that is not finite (its codes become 0)
-__device__ __forceinline__ float inverse_of_byte(uint32_t b) { return __uint_as_float((b == kScaleNan ? 0u : 254u - b) << 23); }
+__device__ __forceinline__ float inverse_of_byte(uint32_t b) {
+    return __uint_as_float((b == kScaleNan ? 0u : 254u - b) << 23);
+}
 
 // Scale bytes from the bits of a block's largest magnitude (any NaN or infinity compares above
 // every finite value).  Adding the carry moves a value above the top code (1.75 or 1.9375 times
@@ -463,8 +465,8 @@ __device__ __forceinline__ void wave_lds_fence() {
 // that one parameter covers is the step above.  Else the blocks' largest magnitudes go through
 // the wavefront's scratch, and only live columns are written.
 template <int DT>
-__device__ __forceinline__ void run8_mixed(const TileMap& M, const AdamK& K, const AdamW8Args& A, RunMax* S, int64_t first,
-                                           int64_t x, int xr, bool in, const float4& g, Run8 q) {
+__device__ __forceinline__ void run8_mixed(const TileMap& M, const AdamK& K, const AdamW8Args& A, RunMax* S,
+                                           int64_t first, int64_t x, int xr, bool in, const float4& g, Run8 q) {
     const int run = xr & ~int(kRun - 1), l4 = xr - run;
     const int64_t block = (x >> kRunShift) + first;
     int k = M.find(xr);
