@@ -48,7 +48,7 @@
  *   stream) and return.  They must be called with the plan's device current.  A plan is
  *   read-only after creation except for the Adam scratch, so hot calls on different
  *   streams are safe when their outputs are disjoint and at most one zero_adam_step per
- *   plan is in flight at a time.
+ *   plan is in flight at a time.  The AdamW calls use a workspace of the caller's instead.
  *
  * Errors:
  *   Every call returns a zero_status and never aborts or prints.  ZERO_EINVAL: a bad
@@ -530,13 +530,16 @@ zero_status zero_adamw_step(const zero_plan* plan, const float* d_g32, float* d_
  *   r: 4 exponent bits of bias 15 and 4 fraction bits, no sign; exponent 0 holds subnormals:
  *      code c stands for (c & 15) 2^-18 if c < 16, else (1 + (c & 15) / 16) 2^((c >> 4) - 15).
  * States of zero bytes are zero.  A step decodes m and r, takes m, v = r^2 and p32 as above (each
- * product and sum of m and v rounded to fp32 by itself), writes p32 and the 16-bit parameter from
- * the unrounded new m and sqrt(v), gives every block of a live parameter the least scale under which
+ * product and sum of m and v rounded to fp32 by itself, the root and the quotient by estimates that
+ * are off by a unit in the last place or two), writes p32 and the 16-bit parameter from the new m
+ * and sqrt(v) before their rounding, gives every block of a live parameter the least scale under which
  * its largest |m| (r) is at most 448 (1.9375), but at least 2^-111 (2^-95), and rounds m and r to
  * the code below or above with a chance that keeps the mean; an r above zero never becomes zero.
  * The chance is decided by a hash of hp->seed, the rank, t and the element's shard column: equal
- * inputs give equal bits.  A block whose new m (r) is not finite everywhere gets scale byte 255
- * and codes 0, and all of it reads as NaN from then on.  States of dead parameters, row gaps and
+ * inputs give equal bits.  A block whose new m (r) is not finite everywhere -- a gradient
+ * that is not, or whose square passes fp32's range (|g| above 1.8e19), in a step that no flag
+ * skips -- gets scale byte 255 and codes 0, and all of it reads as NaN from then on.  Variances
+ * below 2^-126 give roots that are too small.  States of dead parameters, row gaps and
  * skipped steps stay as they were.  Each state element takes 2 bytes and 1/64 instead of 8.
  *   d_m8, d_r8   device uint8[shard_numel], 16-byte aligned
  *   d_scales     device uint8[2 * n_scales], 16-byte aligned; entries that no block has are not used

@@ -8,7 +8,7 @@
 // the schedule's factor, and per parameter the step size, the bias correction and the decay.
 // adamw_kernel then streams the shard: 16 bytes in and 14 out per element, bound by memory (6.35 TB/s on
 // the GPT-2 list at Nd = 8, 920 us; 6.0 TB/s on the 7.5B list at Nd = 64, 578 us, on MI355X; counters:
-// 5.87 GB moved of 5.84 needed).
+// 5.86 GB moved of 5.84 needed).
 #include <cmath>
 
 #include "zs_adamw.h"
