@@ -538,8 +538,8 @@ zero_status zero_adamw_step(const zero_plan* plan, const float* d_g32, float* d_
  * The chance is decided by a hash of hp->seed, the rank, t and the element's shard column: equal
  * inputs give equal bits.  A block whose new m (r) is not finite everywhere -- a gradient
  * that is not, or whose square passes fp32's range (|g| above 1.8e19), in a step that no flag
- * skips -- gets scale byte 255 and codes 0, and all of it reads as NaN from then on.  Variances
- * below 2^-126 give roots that are too small.  States of dead parameters, row gaps and
+ * skips -- gets scale byte 255 and codes 0, and all of it reads as NaN from then on.  The variance
+ * does not leave fp32's range below: r is right down to the least code, 2^-113.  States of dead parameters, row gaps and
  * skipped steps stay as they were.  Each state element takes 2 bytes and 1/64 instead of 8.
  *   d_m8, d_r8   device uint8[shard_numel], 16-byte aligned
  *   d_scales     device uint8[2 * n_scales], 16-byte aligned; entries that no block has are not used

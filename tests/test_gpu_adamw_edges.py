@@ -1,0 +1,125 @@
+"""The AdamW operators at the borders of their ranges: the smallest states that 8 bits hold, a sum of
+squares that another rank made infinite, parameters that are -0 or infinite, the quotient's rounding,
+clipping with 8-bit states and in the fused path, many rows, states that are not numbers."""
+import contextlib
+
+import numpy as np
+import pytest
+import torch
+
+import adamw_reference as R
+import test_gpu_adamw as T
+import zero_sharded_mixed_amd as Z
+from gpu_harness import DEV, ragged_numels, say
+from test_gpu_adamw import Case, check_parameters, close, codes, host
+
+pytestmark = pytest.mark.gpu
+
+
+def states_of(st, bits):
+    return [st.p32, st.arena, st.steps] + ([st.m8, st.r8, st.scales] if bits == 8 else [st.m, st.v])
+
+
+# ----------------------------------------------------------- the smallest 8-bit states ----
+
+def small_states(c, st, first, last):
+    """Random codes (roots not zero) under root scales 2^first .. 2^last and momentum scales as far
+    down; returns the decoded states."""
+    n_scales = st.plan.adamw_n_scales
+    rng = c.rng
+    m8 = rng.integers(0, 256, c.S).astype(np.uint8)
+    m8[(m8 & 127) == 127] = 5
+    r8 = rng.integers(1, 256, c.S).astype(np.uint8)
+    sc = np.stack([rng.integers(first + 119, last + 120, n_scales), rng.integers(first + 127, last + 128, n_scales)], 1)
+    sc = sc.astype(np.uint8).reshape(-1)
+    st.m8, st.r8, st.scales = (torch.from_numpy(a).to(DEV) for a in (m8, r8, sc))
+    return R.decode(m8, r8, sc, c.idx), (m8, r8, sc)
+
+
+def step8_small(ref, i, g32, m, r):
+    """The 8-bit step's new states with fp32 roundings, on values first brought near 1 by a power of
+    two each: what the formula gives where nothing leaves fp32's range."""
+    f = np.float32
+    g = g32.astype(f) * f(ref.mult)
+    m1 = f(ref.b1) * m.astype(f) + f(1 - ref.b1) * g
+    _, e = np.frexp(np.maximum(r, np.abs(g)))
+    rs, gs = np.ldexp(r, -e).astype(f), np.ldexp(g.astype(np.float64), -e).astype(f)
+    r1 = np.sqrt(f(ref.b2) * (rs * rs) + f(1 - ref.b2) * (gs * gs))
+    return m1, np.ldexp(r1.astype(np.float64), e)
+
+
+@pytest.mark.parametrize("gradient", [0.0, 1.0])
+@pytest.mark.parametrize("name", ["mlp", "runs", "ragged-7", "tiny"])
+def test_the_smallest_roots_are_kept(name, gradient):
+    """Roots from 2^-113, the least code under the least scale, to 2^-55, whose squares leave fp32's
+    range, with zero gradients and gradients of their size: codes and scales bit for bit those of the
+    formula, p32 within the bounds of its roundings, with eps far below the roots."""
+    c = Case(name, seed=31)
+    say(f"[small roots] {name} {gradient}")
+    st = c.reset(8)
+    (m0, r0), (m8, r8, sc) = small_states(c, st, -95, -56)
+    g = c.rng.normal(size=c.S) * r0 if gradient else np.zeros(c.S)
+    st.g32 = torch.from_numpy(g.astype(np.float32)).to(DEV)
+    g = host(st.g32)
+    hp = c.hp(seed=5, eps=2.0 ** -126, beta2=0.999, grad_scale=1.0)
+    st.adamw(hp)
+    own, ref = np.maximum(c.own, 0), c.ref(hp)
+    (p, _, _), (ep, _, _) = R.adamw64(ref, own, g, c.p.astype(np.float64), m0, r0 * r0, True)
+    # em and ev of the bounds are relative, and m and the scaled squares stay in the normal range; eps is
+    # the one addend that a root may pass by 2^70
+    check_parameters(c, st, p, ep, name)
+    m1, r1 = step8_small(ref, own, g, m0, r0)
+    h = R.noise(5, c.rank, (c.t + c.live)[own], np.arange(c.S))
+    n_scales = st.plan.adamw_n_scales
+    wm, bm = R.encode(m1, c.idx, c.on, n_scales, "m", h)
+    wr, br = R.encode(r1, c.idx, c.on, n_scales, "r", h)
+    gm, gr, gs = codes(st)
+    old = sc.reshape(-1, 2)
+    assert np.array_equal(gs, np.stack([np.where(bm < 0, old[:, 0], bm), np.where(br < 0, old[:, 1], br)],
+                                       1).reshape(-1).astype(np.uint8))
+    assert np.array_equal(gr, np.where(c.on, wr, r8))
+    assert np.array_equal(gm, np.where(c.on, wm, m8))
+
+
+def test_the_smallest_roots_do_not_vanish_over_steps():
+    """200 steps of zero gradients from roots of 2^-112 .. 2^-60: none becomes zero."""
+    c = Case("runs", seed=32)
+    st = c.reset(8)
+    small_states(c, st, -95, -61)
+    st.g32.fill_(0)
+    for _ in range(200):
+        st.adamw(c.hp(beta2=0.999))
+    assert np.all(host(st.r8)[c.on] > 0)
+
+
+@pytest.mark.parametrize("beta2", [0.999, 0.0])
+@pytest.mark.parametrize("g", [2.0 ** -60, 2.0 ** -120, 2.0 ** -149 * 64])
+def test_a_root_from_the_smallest_gradients_is_not_zero(beta2, g):
+    """A first gradient whose square is zero in fp32, beside states that are zero and (with beta2 = 0)
+    states that the step forgets: the root is sqrt(1 - beta2) |g| up to its rounding to a code."""
+    n = 4096 + 300
+    st = Z.ShardStep([n, 77], 1, 0, 0, Z.ZERO_BF16)
+    if beta2 == 0.0:
+        st.v.fill_(1.0)
+    st.enable_adamw(8)
+    st.g32.fill_(g)
+    st.adamw(Z.AdamWParams(lr=0.0, beta2=beta2))
+    r = st.adamw_states()[1][:n + 77].double().cpu().numpy()
+    want = np.sqrt(1 - beta2) * g
+    least = 2.0 ** -113
+    assert np.all(r >= least) and np.all(np.abs(r - want) <= np.maximum(want / 16, least))
+
+
+def test_a_nan_block_stays_nan_whatever_the_betas():
+    c = Case("runs", seed=40)
+    at = np.flatnonzero(c.on)[100]
+    c.g[at] = np.nan
+    st = c.reset(8)
+    for g in (None, 0.0):
+        if g is not None:
+            st.g32.fill_(g)
+        st.adamw(c.hp(beta1=0.0, beta2=0.0), use_flag=False)
+    m, r = (host(t.float()) for t in st.adamw_states())
+    hit = (c.idx == c.idx[at]) & c.on
+    assert np.isnan(m[hit]).all() and np.isnan(r[hit]).all()
+    assert not np.isnan(m[c.on & ~hit]).any() and not np.isnan(r[c.on & ~hit]).any()

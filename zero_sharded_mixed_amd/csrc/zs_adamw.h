@@ -333,11 +333,25 @@ __device__ __forceinline__ uint32_t root_noise(uint32_t h) { return ((h >> 13) &
 
 // Square root to within a unit in the last place: the reciprocal root's estimate and one Newton
 // step with the exact residual, half the instructions of the correctly rounded sequence, from which
-// it differs once in 10^4 values.  0 gives 0; below 2^-126 it falls short.
+// it differs once in 10^4 values.  0 gives 0; below 2^-126 it falls short (see moved_root).
 __device__ __forceinline__ float root_of(float v) {
     const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));
     const float q = v * y;
     return __builtin_fmaf(__builtin_fmaf(-q, q, v), 0.5f * y, q);
+}
+
+// sqrt(b2 r^2 + c2 g^2).  The states reach down to 2^-113 and gradients to 2^-149, whose squares leave
+// fp32's range, so where the larger of the two lies below 1/2 both are brought to it by a power of two,
+// which is exact: the variance is then at least min(b2, c2) / 4, every rounding is the formula's own
+// without its range, and a root above zero stays above zero.  With beta2 = 0 the old root is dropped
+// first (a NaN stays): beside a gradient far below it, it would not fit.
+__device__ __forceinline__ float moved_root(const AdamK& K, float r, float g) {
+#pragma clang fp contract(off)
+    r *= K.b2 > 0.0f ? 1.0f : 0.0f;
+    const int e = min(__builtin_amdgcn_frexp_expf(fmaxf(r, fabsf(g))), 0);
+    r = __builtin_amdgcn_ldexpf(r, -e);
+    g = __builtin_amdgcn_ldexpf(g, -e);
+    return __builtin_amdgcn_ldexpf(root_of(K.b2 * (r * r) + K.c2 * (g * g)), e);
 }
 
 // One element from the decoded states: new p, m and r, not yet rounded to 8 bits.  Products and
@@ -349,7 +363,7 @@ __device__ __forceinline__ void adamw8_elem(const AdamK& K, const AdamWScal& s, 
 #pragma clang fp contract(off)
     const float g = g32 * K.gs;
     m = K.b1 * m + K.c1 * g;
-    r = root_of(K.b2 * (r * r) + K.c2 * (g * g));
+    r = moved_root(K, r, g);
     p = __builtin_fmaf(-s.shrink, p, p);
     p = __builtin_fmaf(-s.step, m * __builtin_amdgcn_rcpf(__builtin_fmaf(r, s.inv_sqrt_bc2, K.eps)), p);
 }
