@@ -459,11 +459,17 @@ zero_status zero_loss_scaler_update(const int32_t* d_flag, zero_loss_scaler* d_s
  * fused: zero_pack_bucket_check per bucket; zero_adamw_prepare; zero_reduce_adamw_bucket or
  * zero_reduce_adamw8_bucket per bucket.
  *
+ * Every rank has to take a step or skip it alike, but a rank's flag tells of its own part of the
+ * gradient.  So the ranks OR their flags before the step (an all-reduce of one int), or, unfused and
+ * clipped, leave it to the sum: the added *grad_sumsq is not finite as soon as one rank's gradient is
+ * not, and with a d_flag the step then sets the flag and is skipped, on every rank.
+ *
  * Workspace: the calls below that take d_work use zero_adamw_sizes.work_bytes bytes of device
  * memory, 16-byte aligned, owned by the caller, its contents irrelevant before a step.  Calls that
  * may run at the same time (on different streams, or in graphs replayed side by side) need
  * different workspaces; a step's calls must name the same one.  With that, and with disjoint
- * outputs, steps on one plan may overlap: the plan itself is not written. */
+ * outputs (a flag beside a grad_sumsq is one), steps on one plan may overlap: the plan itself is not
+ * written. */
 typedef struct zero_adamw_sizes {
     int64_t work_bytes;   /* bytes of d_work                                              */
     int64_t n_scales;     /* pairs of scale bytes of 8-bit states: 2 * n_scales bytes     */
@@ -476,7 +482,8 @@ zero_status zero_adamw_get_sizes(const zero_plan* plan, zero_adamw_sizes* out);
  * the kernels read when they run.  With mult = grad_scale (/ loss_scaler->scale if given):
  *   norm = sqrt(*grad_sumsq) * |mult|,  coef = max_norm > 0 ? min(1, max_norm / (norm + 1e-6)) : 1,
  *   s = mult * coef (coef 1 without grad_sumsq; NaN if the norm is not finite, so that without
- *   a flag the parameters show it),  lr = hp.lr * *lr_factor,  d_i = decay[i] (1 without decay).
+ *   a flag, which skips such a step, the parameters show it),  lr = hp.lr * *lr_factor,
+ *   d_i = decay[i] (1 without decay).
  * All in double, rounded to fp32 once. */
 typedef struct zero_adamw_hparams {
     double lr;                            /* >= 0                                          */
@@ -503,12 +510,13 @@ typedef struct zero_adamw_hparams {
 zero_status zero_grad_sumsq(const zero_plan* plan, const float* d_g32, const uint8_t* d_live, double* d_sumsq,
                             int32_t* d_flag, void* d_work, void* stream);
 
-/* The first launch of the steps below: if d_flag is NULL or *d_flag == 0, every live parameter's
- * step count advances and the step's scalars are formed in d_work; if the flag is set, nothing
- * changes.  Only the fused path calls it by itself.
+/* The first launch of the steps below: if d_flag is not NULL and *hp->grad_sumsq is not finite, it
+ * ORs 1 into *d_flag.  Then, if d_flag is NULL or *d_flag == 0, every live parameter's step count
+ * advances and the step's scalars are formed in d_work; if the flag is set, nothing else changes.
+ * Only the fused path calls it by itself.
  * Errors: ZERO_EINVAL for NULL or misaligned pointers or hyperparameters out of range. */
 zero_status zero_adamw_prepare(const zero_plan* plan, const uint8_t* d_live, int32_t* d_steps,
-                               const zero_adamw_hparams* hp, const int32_t* d_flag, void* d_work, void* stream);
+                               const zero_adamw_hparams* hp, int32_t* d_flag, void* d_work, void* stream);
 
 /* One AdamW step with 32-bit states.  As zero_adam_step, with for every element e of a live
  * parameter i, t = d_steps[i] after the increment (fp32 arithmetic):
@@ -520,7 +528,7 @@ zero_status zero_adamw_prepare(const zero_plan* plan, const uint8_t* d_live, int
  * Arguments and errors as zero_adam_step, and those of zero_adamw_prepare. */
 zero_status zero_adamw_step(const zero_plan* plan, const float* d_g32, float* d_p32, float* d_m, float* d_v,
                             const uint8_t* d_live, int32_t* d_steps, const zero_adamw_hparams* hp,
-                            const int32_t* d_flag, void* d_arena, void* d_work, void* stream);
+                            int32_t* d_flag, void* d_arena, void* d_work, void* stream);
 
 /* The same step with 8-bit states: the momentum m and the root r of the variance (v = r^2), each
  * a code times a power of two.  A block is the part of one parameter inside one aligned run of
@@ -546,7 +554,7 @@ zero_status zero_adamw_step(const zero_plan* plan, const float* d_g32, float* d_
  * Other arguments and errors as zero_adamw_step. */
 zero_status zero_adamw8_step(const zero_plan* plan, const float* d_g32, float* d_p32, uint8_t* d_m8, uint8_t* d_r8,
                              uint8_t* d_scales, const uint8_t* d_live, int32_t* d_steps,
-                             const zero_adamw_hparams* hp, const int32_t* d_flag, void* d_arena, void* d_work,
+                             const zero_adamw_hparams* hp, int32_t* d_flag, void* d_arena, void* d_work,
                              void* stream);
 
 /* 8-bit states from 32-bit ones (d_m, d_v float[shard_numel]), of every parameter, live or not:

@@ -2,6 +2,7 @@
 squares that another rank made infinite, parameters that are -0 or infinite, the quotient's rounding,
 clipping with 8-bit states and in the fused path, many rows, states that are not numbers."""
 import contextlib
+import ctypes
 
 import numpy as np
 import pytest
@@ -12,6 +13,7 @@ import test_gpu_adamw as T
 import zero_sharded_mixed_amd as Z
 from gpu_harness import DEV, ragged_numels, say
 from test_gpu_adamw import Case, check_parameters, close, codes, host
+from zero_sharded_mixed_amd import _binding as B
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +125,80 @@ def test_a_nan_block_stays_nan_whatever_the_betas():
     hit = (c.idx == c.idx[at]) & c.on
     assert np.isnan(m[hit]).all() and np.isnan(r[hit]).all()
     assert not np.isnan(m[c.on & ~hit]).any() and not np.isnan(r[c.on & ~hit]).any()
+
+
+# ---------------------------------------------- the verdict of a sum that other ranks made infinite ----
+
+@pytest.mark.parametrize("total", [np.inf, np.nan])
+@pytest.mark.parametrize("path", ["unfused", "fused"])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_an_infinite_sum_of_all_ranks_skips_the_step_and_sets_the_flag(bits, path, total):
+    """This rank's gradient is finite and its flag clear; the sum over the ranks is not.  Nothing
+    changes, the flag says so (the loss scale then backs off on every rank), and the next step with a
+    finite sum runs."""
+    c = Case("ragged-7", seed=33)
+    st = c.reset(bits)
+    st.enable_loss_scaler(2.0 ** 8)
+    rows = [(torch.randn(c.nd, int(b.row_stride), device=DEV).mul_(1e-2).bfloat16(), int(b.row_stride))
+            for b in st.buckets]
+
+    def step(extra):
+        st.reduce(lambda b: rows[b])
+        st.grad_sumsq()
+        st.sumsq += extra  # the other ranks' sums
+        hp = c.hp(max_norm=1.0, seed=3, grad_sumsq=st.sumsq, norm_out=st.norm_out)
+        if path == "fused":
+            st.reduce_adamw(lambda b: rows[b], hp)
+        else:
+            st.adamw(hp)
+
+    before = [t.clone() for t in states_of(st, bits)]
+    st.norm_out.fill_(-1)
+    step(total)
+    assert int(st.flag) == 1
+    assert all(torch.equal(a, b) for a, b in zip(states_of(st, bits), before))
+    assert st.norm_out.tolist() == [-1, -1]
+    st.update_loss_scale()
+    assert float(Z.read_loss_scaler(st.scaler).scale) == 2.0 ** 7
+    st.flag.zero_()
+    step(1.0)
+    assert int(st.flag) == 0 and np.array_equal(host(st.steps), c.t + c.live)
+    assert np.isfinite(host(st.p32)[c.on]).all()
+
+
+def test_ranks_agree_on_a_skipped_step():
+    """Two ranks, one with an infinite gradient in its shard: with the sums added both skip, both back
+    their loss scales off, and both take the next step with the same norm."""
+    n = [3000, 5001]
+    ranks = [Z.ShardStep(n, 2, k, 0, Z.ZERO_FP16) for k in range(2)]
+    for k, st in enumerate(ranks):
+        st.enable_adamw(8 if k else 32)
+        st.enable_loss_scaler(2.0 ** 10)
+        st.p32.fill_(0.5)
+    for turn, bad in enumerate((float("inf"), 1.0)):
+        for k, st in enumerate(ranks):
+            st.flag.zero_()
+            st.g32.fill_(0.25 * 2.0 ** 10)
+            st.g32[17] = bad if k == 0 else 1.0
+            st.grad_sumsq()
+        total = ranks[0].sumsq + ranks[1].sumsq
+        for st in ranks:
+            st.sumsq.copy_(total)
+            st.adamw(Z.AdamWParams(lr=1e-3, max_norm=1.0))
+        assert [int(st.flag) for st in ranks] == [1 - turn] * 2
+        for st in ranks:
+            st.update_loss_scale()
+            assert float(Z.read_loss_scaler(st.scaler).scale) == 2.0 ** 9
+            assert st.steps.tolist() == [turn, turn] and bool(torch.isfinite(st.p32).all())
+            assert bool((st.p32 == 0.5).all()) == (turn == 0)
+    assert torch.equal(ranks[0].norm_out, ranks[1].norm_out)
+
+
+def test_a_misaligned_flag_is_refused():
+    c = Case("mlp", seed=41)
+    st = c.reset()
+    hp = B._adamw_hp(st.plan, c.hp(), "hp")
+    at = lambda t, k=0: ctypes.c_void_p(t.data_ptr() + k)  # noqa: E731
+    args = [st.plan.handle, at(st.live), at(st.steps), ctypes.byref(hp)]
+    assert Z.lib().zero_adamw_prepare(*args, at(st.flag, 2), at(st.work), None) == Z.ZERO_EINVAL
+    assert "flag" in Z.zero_last_error()

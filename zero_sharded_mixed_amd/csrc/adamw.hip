@@ -3,7 +3,7 @@
 // launch that the 32-bit, the 8-bit and the fused steps share.
 //
 // Two launches, as for zero_adam_step.  adamw_prepare_kernel (one thread per parameter) reads the
-// overflow flag, advances the live parameters' step counts and forms every scalar of the step in
+// overflow flag (and sets it where the sum of squares of all ranks is not finite), advances the live parameters' step counts and forms every scalar of the step in
 // double: the clip coefficient from the sum of squares, the gradient multiplier, the rate from
 // the schedule's factor, and per parameter the step size, the bias correction and the decay.
 // adamw_kernel then streams the shard: 16 bytes in and 14 out per element, bound by memory (6.35 TB/s on
@@ -26,10 +26,17 @@ struct AdamWHost {  // the hyperparameters by value, and the rounding noise's ke
 };
 
 __global__ void adamw_prepare_kernel(DevPlan P, const uint8_t* __restrict__ live, int32_t* __restrict__ steps,
-                                     const int32_t* __restrict__ flag, AdamWHost H, float4* __restrict__ scal,
+                                     int32_t* flag, AdamWHost H, float4* __restrict__ scal,
                                      float* __restrict__ consts) {
-    if (flag && *flag) return;
     const int64_t gid = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
+    if (flag) {
+        // The sum over the ranks is not finite on every rank as soon as one rank's gradient is not, while
+        // only that rank's flag is set: all of them skip the step, and their flags say so to what
+        // follows (the step's other launches, the loss scale).
+        const bool lost = H.sumsq && !(fabs(*H.sumsq) < __builtin_inf());
+        if (lost && gid == 0) atomicOr(flag, 1);
+        if (lost || *flag) return;
+    }
     if (gid == 0) {
         double mult = H.scaler ? H.grad_scale / double(H.scaler->scale) : H.grad_scale;
         if (H.sumsq) {
@@ -150,11 +157,12 @@ zero_status check_work(const void* work, const char* who) {
 }
 
 zero_status launch_adamw_prepare(const zero_plan* plan, const uint8_t* d_live, int32_t* d_steps,
-                                 const zero_adamw_hparams* hp, const int32_t* d_flag, void* work, hipStream_t s,
+                                 const zero_adamw_hparams* hp, int32_t* d_flag, void* work, hipStream_t s,
                                  const char* who) {
     if (!d_live || !d_steps || !hp) return fail(ZERO_EINVAL, "%s: NULL pointer", who);
     const zero_status st = check_work(work, who);
     if (st != ZERO_OK) return st;
+    if (reinterpret_cast<uintptr_t>(d_flag) % 4 != 0) return fail(ZERO_EINVAL, "%s: flag not 4-byte aligned", who);
     const auto at_least_0 = [](double x) { return std::isfinite(x) && x >= 0.0; };
     if (!at_least_0(hp->lr) || !(hp->beta1 >= 0.0) || !(hp->beta1 < 1.0) || !(hp->beta2 >= 0.0) || !(hp->beta2 < 1.0) ||
         !at_least_0(hp->weight_decay) || !std::isfinite(hp->grad_scale) || !at_least_0(hp->max_norm))
@@ -190,7 +198,7 @@ extern "C" zero_status zero_adamw_get_sizes(const zero_plan* plan, zero_adamw_si
 }
 
 extern "C" zero_status zero_adamw_prepare(const zero_plan* plan, const uint8_t* d_live, int32_t* d_steps,
-                                          const zero_adamw_hparams* hp, const int32_t* d_flag, void* d_work,
+                                          const zero_adamw_hparams* hp, int32_t* d_flag, void* d_work,
                                           void* stream) {
     const zero_status st = check_device(plan);
     if (st != ZERO_OK) return st;
@@ -199,7 +207,7 @@ extern "C" zero_status zero_adamw_prepare(const zero_plan* plan, const uint8_t* 
 
 extern "C" zero_status zero_adamw_step(const zero_plan* plan, const float* d_g32, float* d_p32, float* d_m, float* d_v,
                                        const uint8_t* d_live, int32_t* d_steps, const zero_adamw_hparams* hp,
-                                       const int32_t* d_flag, void* d_arena, void* d_work, void* stream) {
+                                       int32_t* d_flag, void* d_arena, void* d_work, void* stream) {
     const char* who = "zero_adamw_step";
     zero_status st = check_device(plan);
     if (st != ZERO_OK) return st;

@@ -195,7 +195,7 @@ using namespace zs;
 
 extern "C" zero_status zero_adamw8_step(const zero_plan* plan, const float* d_g32, float* d_p32, uint8_t* d_m8,
                                         uint8_t* d_r8, uint8_t* d_scales, const uint8_t* d_live, int32_t* d_steps,
-                                        const zero_adamw_hparams* hp, const int32_t* d_flag, void* d_arena,
+                                        const zero_adamw_hparams* hp, int32_t* d_flag, void* d_arena,
                                         void* d_work, void* stream) {
     const char* who = "zero_adamw8_step";
     zero_status st = check_device(plan);

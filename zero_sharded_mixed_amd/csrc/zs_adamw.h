@@ -553,7 +553,7 @@ __device__ __forceinline__ void run8_mixed(const TileMap& M, const AdamK& K, con
 
 // Checks of a step's hyperparameters, and the prepare launch into `work` (adamw.hip).
 zero_status launch_adamw_prepare(const zero_plan* plan, const uint8_t* d_live, int32_t* d_steps,
-                                 const zero_adamw_hparams* hp, const int32_t* d_flag, void* work, hipStream_t s,
+                                 const zero_adamw_hparams* hp, int32_t* d_flag, void* work, hipStream_t s,
                                  const char* who);
 zero_status check_work(const void* work, const char* who);
 

@@ -166,7 +166,9 @@ class ShardStep:
 
     def adamw(self, hp: B.AdamWParams, use_flag: bool = True, stream=None) -> None:
         """One AdamW step on self.g32.  With hp.max_norm > 0 the norm comes from grad_sumsq(), and
-        self.norm_out receives it and the clip coefficient.  A captured graph reads hp's tensors at
+        self.norm_out receives it and the clip coefficient.  use_flag=True: a set self.flag skips the
+        step, and a sum of squares that is not finite sets it (on every rank that has the sum); without
+        such a sum the ranks OR their flags before the step.  A captured graph reads hp's tensors at
         every replay: keep hp for as long as the graph."""
         hp, flag = self._adamw_params(hp), self.flag if use_flag else None
         if self.adamw_bits == 8:
