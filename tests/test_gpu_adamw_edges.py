@@ -202,3 +202,41 @@ def test_a_misaligned_flag_is_refused():
     args = [st.plan.handle, at(st.live), at(st.steps), ctypes.byref(hp)]
     assert Z.lib().zero_adamw_prepare(*args, at(st.flag, 2), at(st.work), None) == Z.ZERO_EINVAL
     assert "flag" in Z.zero_last_error()
+
+
+# -------------------------------------------------------- parameters that are -0 or infinite ----
+
+SPECIAL = np.array([-0.0, 0.0, np.inf, -np.inf, np.nan, 2.0 ** -149, -2.0 ** -149, 3e38], np.float32)
+
+
+@pytest.mark.parametrize("how", ["weight_decay", "decay", "lr"])
+@pytest.mark.parametrize("name", ["mlp", "ragged-7", "tiny"])
+def test_without_decay_special_parameters_have_adam_s_bits(name, how):
+    """-0, infinities and NaN among the parameters, half of the gradients and states zero: the bits of
+    the Adam step, whether the decay is zero by the rate, the weight or the parameter's multiplier."""
+    c = Case(name, seed=34)
+    c.p[:] = c.rng.choice(SPECIAL, c.S)
+    zero = c.rng.random(c.S) < 0.5
+    c.g[zero], c.m[zero], c.v[zero] = 0, 0, 0
+    lr = 0.0 if how == "lr" else 2e-3
+    kw = dict(lr=lr, weight_decay=0.0 if how == "weight_decay" else 0.1)
+    if how == "decay":
+        kw["decay"] = torch.zeros(c.n, device=DEV)
+    a = c.reset()
+    a.adamw(c.hp(**kw))
+    got = [a.p32, a.m, a.v, a.steps, a.arena]
+    b = c.reset()
+    b.adam(lr, 0.9, 0.99, 1e-8, 1.0 / c.nd)
+    for x, y in zip(got, [b.p32, b.m, b.v, b.steps, b.arena]):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
+@pytest.mark.parametrize("name", ["mlp", "ragged-7", "tiny"])
+def test_without_decay_special_parameters_stay_in_the_8_bit_step(name):
+    """Zero gradients, zero states, no decay: p32 keeps its bits, also with decay for others."""
+    c = Case(name, seed=35)
+    c.p[:] = c.rng.choice(SPECIAL[[0, 1, 2, 3, 5, 6, 7]], c.S)
+    c.g[:], c.m[:], c.v[:] = 0, 0, 0
+    st = c.reset(8)
+    st.adamw(c.hp(decay=torch.zeros(c.n, device=DEV)))
+    assert np.array_equal(host(st.p32).view(np.uint32), c.p.view(np.uint32))

@@ -139,10 +139,16 @@ __device__ __forceinline__ void mixed_tile(TileMap& M, const DevPlan& P, const f
 }
 
 // ------------------------------------------------------------------------- 32-bit states --
-// One element in fp32 with every rounding spelled out.  Without decay (shrink = 0) the bits are
-// those of adam_elem: fma(-0, p, p) is p.
+// p less its decay.  Without decay (shrink = 0) every p keeps its bits: fma(-0, p, p) would turn -0 into
+// 0 and an infinity into NaN.
+__device__ __forceinline__ float decayed(const AdamWScal& s, float p) {
+    const float q = __builtin_fmaf(-s.shrink, p, p);
+    return s.shrink == 0.0f ? p : q;
+}
+
+// One element in fp32 with every rounding spelled out.  Without decay the bits are those of adam_elem.
 __device__ __forceinline__ void adamw_elem(const AdamK& K, const AdamWScal& s, float g32, float& p, float& m, float& v) {
-    p = __builtin_fmaf(-s.shrink, p, p);
+    p = decayed(s, p);
     adam_elem(K, g32, p, m, v, s.step, s.inv_sqrt_bc2);
 }
 
@@ -364,7 +370,7 @@ __device__ __forceinline__ void adamw8_elem(const AdamK& K, const AdamWScal& s, 
     const float g = g32 * K.gs;
     m = K.b1 * m + K.c1 * g;
     r = moved_root(K, r, g);
-    p = __builtin_fmaf(-s.shrink, p, p);
+    p = decayed(s, p);
     p = __builtin_fmaf(-s.step, m * __builtin_amdgcn_rcpf(__builtin_fmaf(r, s.inv_sqrt_bc2, K.eps)), p);
 }
 
