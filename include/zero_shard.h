@@ -488,7 +488,7 @@ zero_status zero_adamw_get_sizes(const zero_plan* plan, zero_adamw_sizes* out);
 typedef struct zero_adamw_hparams {
     double lr;                            /* >= 0                                          */
     double beta1, beta2;                  /* in [0, 1)                                     */
-    double eps;                           /* finite, >= 2^-126                             */
+    double eps;                           /* >= 2^-126, finite in fp32                      */
     double weight_decay;                  /* >= 0                                          */
     double grad_scale;                    /* as zero_adam_hparams                          */
     double max_norm;                      /* >= 0; 0 = no clipping; > 0 needs grad_sumsq   */
@@ -538,11 +538,12 @@ zero_status zero_adamw_step(const zero_plan* plan, const float* d_g32, float* d_
  *   r: 4 exponent bits of bias 15 and 4 fraction bits, no sign; exponent 0 holds subnormals:
  *      code c stands for (c & 15) 2^-18 if c < 16, else (1 + (c & 15) / 16) 2^((c >> 4) - 15).
  * States of zero bytes are zero.  A step decodes m and r, takes m, v = r^2 and p32 as above (each
- * product and sum of m and v rounded to fp32 by itself, the root and the quotient by estimates that
- * are off by a unit in the last place or two), writes p32 and the 16-bit parameter from the new m
- * and sqrt(v) before their rounding, gives every block of a live parameter the least scale under which
- * its largest |m| (r) is at most 448 (1.9375), but at least 2^-111 (2^-95), and rounds m and r to
- * the code below or above with a chance that keeps the mean; an r above zero never becomes zero.
+ * product and sum of m and v rounded to fp32 by itself, the root and the quotient by an estimate and a
+ * correction, off by little more than half a unit in the last place), writes p32 and the 16-bit
+ * parameter from the new m and sqrt(v) before their rounding, gives every block of a live parameter the
+ * least scale under which its largest |m| (r) is at most 448 (1.9375), but at least 2^-111 (2^-95), and
+ * rounds m and r to the code below or above with a chance that keeps the mean; an r above zero never
+ * becomes zero.
  * The chance is decided by a hash of hp->seed, the rank, t and the element's shard column: equal
  * inputs give equal bits.  A block whose new m (r) is not finite everywhere -- a gradient
  * that is not, or whose square passes fp32's range (|g| above 1.8e19), in a step that no flag

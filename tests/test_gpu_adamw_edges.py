@@ -240,3 +240,34 @@ def test_without_decay_special_parameters_stay_in_the_8_bit_step(name):
     st = c.reset(8)
     st.adamw(c.hp(decay=torch.zeros(c.n, device=DEV)))
     assert np.array_equal(host(st.p32).view(np.uint32), c.p.view(np.uint32))
+
+
+# ------------------------------------------------------------------ the quotient's rounding ----
+
+def test_the_8_bit_step_s_quotient_is_the_nearest():
+    """beta1 = beta2 = 0, lr = 1, p = 0: p becomes -g / (|g| + eps) with one rounding, every g = k / 4096
+    (its square, its root and the sum with eps = 1/2 are exact).  The quotient k / (k + 2048) of a 12-bit
+    by a 13-bit integer d stays at least 1 / (2 d) > 2^-14 of fp32's spacing away from the middle of
+    two neighbours, and a residual's correction leaves an error of 2^-21 of it: the result is the
+    nearest."""
+    k = np.arange(1, 4096)
+    g = (k / 4096).astype(np.float32)
+    g[::2] *= -1
+    st = Z.ShardStep([g.size], 1, 0, 0, Z.ZERO_BF16)
+    st.enable_adamw(8)
+    st.g32[:g.size] = torch.from_numpy(g).to(DEV)
+    st.adamw(Z.AdamWParams(lr=1.0, beta1=0.0, beta2=0.0, eps=0.5))
+    got = host(st.p32)[:g.size]
+    want = (-g.astype(np.float64) / (np.abs(g.astype(np.float64)) + 0.5)).astype(np.float32)
+    off = got.view(np.int32).astype(np.int64) - want.view(np.int32)
+    assert not off.any(), f"{(off != 0).sum()} of {off.size} quotients, by up to {np.abs(off).max()} units"
+
+
+def test_eps_outside_fp32_is_refused():
+    st = Z.ShardStep([64], 1, 0, 0, Z.ZERO_BF16)
+    st.enable_adamw()
+    for eps in (1e39, 2.0 ** -127):
+        with pytest.raises(Z.ZeroError, match="eps"):
+            st.adamw(Z.AdamWParams(lr=1e-3, eps=eps))
+    st.adamw(Z.AdamWParams(lr=1e-3, eps=3e38))
+    assert not st.p32.any()

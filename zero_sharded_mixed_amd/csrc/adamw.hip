@@ -168,8 +168,8 @@ zero_status launch_adamw_prepare(const zero_plan* plan, const uint8_t* d_live, i
         !at_least_0(hp->weight_decay) || !std::isfinite(hp->grad_scale) || !at_least_0(hp->max_norm))
         return fail(ZERO_EINVAL, "%s: hyperparameters out of range", who);
     // eps keeps the padding's update, 0 / (0 + eps), a number, and its reciprocal finite
-    if (!std::isfinite(hp->eps) || !(float(hp->eps) >= 0x1p-126f))
-        return fail(ZERO_EINVAL, "%s: eps must be at least fp32's smallest normal number", who);
+    if (!std::isfinite(float(hp->eps)) || !(float(hp->eps) >= 0x1p-126f))
+        return fail(ZERO_EINVAL, "%s: eps must be a normal number of fp32, above zero", who);
     if (!hp->grad_sumsq && (hp->max_norm > 0.0 || hp->norm_out))
         return fail(ZERO_EINVAL, "%s: max_norm and norm_out need grad_sumsq", who);
     if (reinterpret_cast<uintptr_t>(hp->grad_sumsq) % 8 != 0 ||

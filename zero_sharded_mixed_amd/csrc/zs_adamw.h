@@ -360,18 +360,28 @@ __device__ __forceinline__ float moved_root(const AdamK& K, float r, float g) {
     return __builtin_amdgcn_ldexpf(root_of(K.b2 * (r * r) + K.c2 * (g * g)), e);
 }
 
+// m / den: the product with the reciprocal's estimate (off by a unit or two) and one correction by the
+// exact residual, which leaves the nearest value, but for one in 2^20 that lies next to the middle.
+// Where |m| < 2^-102 the residual loses bits below fp32's range, and the product's unit stays.  den is
+// finite and at least 2^-126, as eps is.
+__device__ __forceinline__ float quotient_of(float m, float den) {
+    const float y = __builtin_amdgcn_rcpf(den);
+    const float q = m * y;
+    return __builtin_fmaf(__builtin_fmaf(-q, den, m), y, q);
+}
+
 // One element from the decoded states: new p, m and r, not yet rounded to 8 bits.  Products and
 // sums of m and v are rounded one by one, no contraction: a value next to a code's border then
-// falls on the side that the formula in fp32 gives.  The quotient is m times the reciprocal's
-// estimate (a unit): with a division and a root correctly rounded the step's arithmetic takes as
-// long as its memory traffic, and both round the update, not the state.
+// falls on the side that the formula in fp32 gives.  The root and the quotient are an estimate and
+// one correction each: with the compiler's correctly rounded sequences the step's arithmetic takes as
+// long as its memory traffic.
 __device__ __forceinline__ void adamw8_elem(const AdamK& K, const AdamWScal& s, float g32, float& p, float& m, float& r) {
 #pragma clang fp contract(off)
     const float g = g32 * K.gs;
     m = K.b1 * m + K.c1 * g;
     r = moved_root(K, r, g);
     p = decayed(s, p);
-    p = __builtin_fmaf(-s.step, m * __builtin_amdgcn_rcpf(__builtin_fmaf(r, s.inv_sqrt_bc2, K.eps)), p);
+    p = __builtin_fmaf(-s.step, quotient_of(m, __builtin_fmaf(r, s.inv_sqrt_bc2, K.eps)), p);
 }
 
 // Largest of a value over the 64 lanes (every lane active), in a scalar register: shifts within
