@@ -46,6 +46,7 @@ class ShardStep:
         self.arena = torch.zeros(int(s.arena_numel), dtype=torch.int16, device=self.device)
         self.scaler: Optional[torch.Tensor] = None  # device zero_loss_scaler, once enabled
         self.adamw_bits = 0  # 32 or 8 once enable_adamw() has been called
+        self.sum_formed = False  # self.sumsq belongs to the gradient in self.g32
 
     def enable_loss_scaler(self, scale: float, growth_interval: int = 2000, growth_factor: float = 2.0,
                            backoff_factor: float = 0.5, min_scale: float = 1.0, max_scale: float = 2.0 ** 24,
@@ -70,7 +71,8 @@ class ShardStep:
         dev = self.device
         if not self.adamw_bits:
             self.work = torch.zeros(self.plan.adamw_work_bytes, dtype=torch.uint8, device=dev)
-            self.sumsq = torch.zeros(1, dtype=torch.float64, device=dev)
+            self.sumsq = torch.full((1,), float("nan"), dtype=torch.float64, device=dev)  # no sum yet
+            self.sum_formed = False
             self.norm_out = torch.zeros(2, dtype=torch.float32, device=dev)
         if bits == 8 and self.adamw_bits != 8:
             S = int(self.summary.shard_numel)
@@ -116,6 +118,7 @@ class ShardStep:
 
     def reduce(self, rows_of: Callable[[int], tuple], fused_check: bool = True, stream=None) -> None:
         """rows_of(b) -> (tensor starting at row 0 of bucket b, row stride in elements)."""
+        self.sum_formed = False
         for b in range(len(self.buckets)):
             rows, stride = rows_of(b)
             B.zero_reduce_shard(self.plan, b, rows, stride, self.live, self.g32,
@@ -146,6 +149,7 @@ class ShardStep:
         adamw()).  check=True: also OR "not finite" into self.flag."""
         self._need_adamw()
         B.zero_grad_sumsq(self.plan, self.g32, self.live, self.sumsq, self.work, self.flag if check else None, stream)
+        self.sum_formed = True
         return self.sumsq
 
     def _need_adamw(self) -> None:
@@ -159,6 +163,8 @@ class ShardStep:
         if hp.loss_scaler is None and self.scaler is not None:
             own["loss_scaler"] = self.scaler
         if hp.max_norm > 0 and hp.grad_sumsq is None:
+            if not self.sum_formed:
+                raise ValueError("adamw: clipping needs grad_sumsq() after the reduce, or a sum in hp.grad_sumsq")
             own["grad_sumsq"] = self.sumsq
             if hp.norm_out is None:
                 own["norm_out"] = self.norm_out
@@ -166,7 +172,8 @@ class ShardStep:
 
     def adamw(self, hp: B.AdamWParams, use_flag: bool = True, stream=None) -> None:
         """One AdamW step on self.g32.  With hp.max_norm > 0 the norm comes from grad_sumsq(), and
-        self.norm_out receives it and the clip coefficient.  use_flag=True: a set self.flag skips the
+        self.norm_out receives it and the clip coefficient; without grad_sumsq() since the last reduce
+        (and without a sum in hp.grad_sumsq) the step is refused: the sum would be another gradient's.  use_flag=True: a set self.flag skips the
         step, and a sum of squares that is not finite sets it (on every rank that has the sum); without
         such a sum the ranks OR their flags before the step.  A captured graph reads hp's tensors at
         every replay: keep hp for as long as the graph."""
@@ -370,6 +377,7 @@ class Zero3Schedule:
         rows_of(l): (rows of bucket l from the Nd ranks, row stride) for the reduce-scatter;
         out: where the packed gradient blocks go (arena layout; default st.packed)."""
         st = self.st
+        st.sum_formed = False
         out = st.packed if out is None else out
         last = len(self.layers) - 1
         if self.fused:
