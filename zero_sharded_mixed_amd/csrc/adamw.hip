@@ -86,11 +86,13 @@ struct AdamWArgs {
     uint16_t* arena;
 };
 
-// From this many tiles on, the kernel reserves LDS for two blocks per CU (kTwoBlocksLds).  Measured
+// From this many tiles on, the kernel reserves LDS for two blocks per CU (two_blocks_lds).  Measured
 // on MI355X, reserved against not: 22.9 us against 18.4 on the ragged list's 1270 tiles,
 // 46 both at 4.0K tiles of the GPT-2 list, 81 against 80 at 7.9K, 159 against 165 at 15.8K, 312
 // against 320 at 31.7K, 919 against 925 at 95K.
 constexpr int64_t kManyTiles = 12 * 1024;
+constexpr unsigned kManyTilesLds = two_blocks_lds(sizeof(TileMap));  // beside the kernel's own map
+static_assert(kManyTilesLds + sizeof(TileMap) <= kBlockLdsMax, "within the LDS limit of a block");
 
 // One block per tile of 2048 columns, lane-strided, every load and store in whole lines and
 // nontemporal.  In a tile inside one parameter the scalars are uniform, and the two quads of a
@@ -223,7 +225,7 @@ extern "C" zero_status zero_adamw_step(const zero_plan* plan, const float* d_g32
     const AdamWArgs A{d_g32, d_p32, d_m, d_v, work_scal(d_work), work_consts(d_work), d_flag,
                       static_cast<uint16_t*>(d_arena)};
     const int g = grid_for(plan->dev.n_tiles);
-    const unsigned lds = plan->dev.n_tiles >= kManyTiles ? kTwoBlocksLds : 0u;
+    const unsigned lds = plan->dev.n_tiles >= kManyTiles ? kManyTilesLds : 0u;
     if (plan->dtype == ZERO_BF16) adamw_kernel<ZERO_BF16><<<g, kBlock, lds, s>>>(plan->dev, A);
     else adamw_kernel<ZERO_FP16><<<g, kBlock, lds, s>>>(plan->dev, A);
     return check_launch(who);

@@ -26,6 +26,10 @@ constexpr int64_t kManyRows = 48, kManyRows8 = 24;
 // Reserved where fewer blocks are faster: with the kernels' own 16 and 24 KB, four and three blocks
 // fit a CU's 160 KB.
 constexpr unsigned kFewBlocksLds = 16 * 1024;
+constexpr int64_t kBlockLds = kTileCols * 4 + sizeof(TileMap) + kFewBlocksLds;
+constexpr int64_t kBlockLds8 = kBlockLds + kBlock / 64 * sizeof(RunMax);
+static_assert(4 * kBlockLds <= kLdsPerCu && 5 * kBlockLds > kLdsPerCu, "four blocks per CU");
+static_assert(3 * kBlockLds8 <= kLdsPerCu && 4 * kBlockLds8 > kLdsPerCu, "three blocks per CU");
 
 // A tile inside one live parameter: every thread sums 8 columns in a row (16-byte loads of every
 // rank's row), the sums go through LDS, and the step takes the tile lane-strided.  The tile's

@@ -29,6 +29,10 @@ inline int grid_for(int64_t work, int64_t cap = ZS_GRID_CAP) {
 constexpr int64_t kLdsPerCu = 160 * 1024;
 constexpr unsigned kTwoBlocksLds = 60 * 1024;
 static_assert(2 * kTwoBlocksLds <= kLdsPerCu && 3 * kTwoBlocksLds > kLdsPerCu, "two blocks per CU");
-static_assert(kTwoBlocksLds <= 64 * 1024, "within the default dynamic LDS limit of a block");
+constexpr unsigned kBlockLdsMax = 64 * 1024;  // LDS of a block, its own and reserved, without raising the limit
+static_assert(kTwoBlocksLds <= kBlockLdsMax, "within the default LDS limit of a block");
+// The bytes to reserve for a kernel that holds `own` bytes of LDS itself, so that both together are
+// kTwoBlocksLds.
+constexpr unsigned two_blocks_lds(unsigned own) { return own < kTwoBlocksLds ? kTwoBlocksLds - own : 0; }
 
 }  // namespace zs
