@@ -16,15 +16,6 @@
 
 #include "zs_adamw.h"
 
-#ifndef LOADS_FIRST
-#define LOADS_FIRST
-#endif
-#ifndef AB
-#define AB 1
-#endif
-#ifndef ALDS
-#define ALDS 0
-#endif
 namespace zs {
 
 // First column of column x's run.
