@@ -271,3 +271,139 @@ def test_eps_outside_fp32_is_refused():
             st.adamw(Z.AdamWParams(lr=1e-3, eps=eps))
     st.adamw(Z.AdamWParams(lr=1e-3, eps=3e38))
     assert not st.p32.any()
+
+
+# -------------------------------------------------------- clipping, loss scale and schedule ----
+
+@pytest.mark.parametrize("dtype", [Z.ZERO_BF16, Z.ZERO_FP16])
+@pytest.mark.parametrize("max_norm", [0.0, 1e-4, 1e9])
+@pytest.mark.parametrize("name", ["mlp", "ragged-7"])
+def test_adamw8_under_clip_scale_and_schedule(name, max_norm, dtype):
+    """The 8-bit step with a sum of squares, a loss scale and a rate factor: parameters, codes and
+    scales, not the norm alone."""
+    c = Case(name, dtype, seed=36)
+    st = c.reset(8)
+    st.enable_loss_scaler(2.0 ** 10)
+    factor = torch.full((1,), 0.3, device=DEV)
+    st.grad_sumsq()
+    sumsq = float(st.sumsq)
+    m8, r8, sc = codes(st)
+    m0, r0 = R.decode(m8, r8, sc, c.idx)
+    hp = c.hp(max_norm=max_norm, lr_factor=factor, grad_sumsq=st.sumsq, norm_out=st.norm_out, seed=17)
+    st.adamw(hp)
+    own, ref = np.maximum(c.own, 0), c.ref(hp, sumsq=sumsq, scale=2.0 ** 10, lr_factor=0.3)
+    (p, _, _), (ep, _, _) = R.adamw64(ref, own, c.g, c.p.astype(np.float64), m0, r0 * r0, True)
+    check_parameters(c, st, p, ep, name)
+    m1, r1 = R.adamw8_f32(ref, own, c.g, m0, r0)
+    h = R.noise(17, c.rank, (c.t + c.live)[own], np.arange(c.S))
+    wm, bm = R.encode(m1, c.idx, c.on, st.plan.adamw_n_scales, "m", h)
+    wr, br = R.encode(r1, c.idx, c.on, st.plan.adamw_n_scales, "r", h)
+    old = sc.reshape(-1, 2)
+    want = np.stack([np.where(bm < 0, old[:, 0], bm), np.where(br < 0, old[:, 1], br)], 1).reshape(-1)
+    gm, gr, gs = codes(st)
+    assert np.array_equal(gs, want.astype(np.uint8))
+    assert np.array_equal(gm, np.where(c.on, wm, m8)) and np.array_equal(gr, np.where(c.on, wr, r8))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype", [Z.ZERO_BF16, Z.ZERO_FP16])
+@pytest.mark.parametrize("name", ["mlp", "ragged-7", "ragged-64"])
+def test_the_fused_step_takes_clip_scale_and_schedule(name, dtype, bits):
+    """The unfused step forms the norm; the fused one is given the same sum: the same bits, with a
+    coefficient below 1, a loss scale that changes between the steps and a rate factor."""
+    c = Case(name, dtype, seed=37)
+    rows = [((torch.randn(c.nd, int(b.row_stride), device=DEV) * 1e-2).to(T.TORCH16[dtype]), int(b.row_stride))
+            for b in c.st.buckets]
+    factor = torch.full((1,), 0.3, device=DEV)
+    sums, got = [], []
+    for fused in (False, True):
+        st = c.reset(bits)
+        st.enable_loss_scaler(2.0 ** 4, growth_interval=1)
+        norms = []
+        for k in range(2):
+            if fused:
+                hp = c.hp(seed=5, max_norm=1e-3, lr_factor=factor, grad_sumsq=sums[k], norm_out=st.norm_out)
+                st.reduce_adamw(lambda b: rows[b], hp)
+            else:
+                st.reduce(lambda b: rows[b])
+                sums.append(st.grad_sumsq().clone())
+                st.adamw(c.hp(seed=5, max_norm=1e-3, lr_factor=factor))
+            norms.append(st.norm_out.clone())
+            st.update_loss_scale()
+        assert 0 < float(norms[0][1]) < 1 and float(norms[1][0]) == float(norms[0][0]) / 2
+        got.append(states_of(st, bits) + norms)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+# -------------------------------------------------------------------------- many rows, load ----
+
+@contextlib.contextmanager
+def layout(name, *what):
+    T.LISTS[name] = what
+    try:
+        yield name
+    finally:
+        del T.LISTS[name]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype", [Z.ZERO_BF16, Z.ZERO_FP16])
+@pytest.mark.parametrize("nd", [65, 100, 1024])
+def test_the_fused_step_over_many_rows_has_the_same_bits(nd, dtype, bits):
+    """Row counts above 64, whole tiles and tiles of several parameters, the last group of rows full
+    and not."""
+    rng = np.random.default_rng(nd)
+    numels = [nd * 5000] + ragged_numels(rng, 60, nd, 40 * nd) + [nd * 2048 * 2]
+    with layout("rows", numels, nd, nd - 1, 2 * 12000 * nd) as name:
+        c = Case(name, dtype, seed=38)
+    say(f"[rows] {nd} {dtype} {bits}: {c.S} columns, {len(c.st.buckets)} buckets")
+    rows = []
+    for b in c.st.buckets:
+        stride = int(b.row_stride) + 8
+        rows.append(((torch.randn(nd, stride, device=DEV) * 1e-2).to(T.TORCH16[dtype]), stride))
+    got = []
+    for fused in (False, True):
+        st = c.reset(bits)
+        if fused:
+            st.reduce_adamw(lambda b: rows[b], c.hp(seed=5))
+        else:
+            st.reduce(lambda b: rows[b])
+            st.adamw(c.hp(seed=5))
+        got.append(states_of(st, bits))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["mlp", "runs", "ragged-7", "tiny"])
+def test_load_of_states_that_are_not_finite(name):
+    """NaN and infinite states, variances below zero, -0 and fp32's subnormals: a block with a value
+    that is not finite (the root of a variance below zero is NaN) has scale 255 and codes 0, the
+    others the nearest codes."""
+    c = Case(name, seed=39)
+    hit = c.rng.random(c.S)
+    for k, x in enumerate((np.nan, np.inf, -np.inf)):
+        c.m[(hit > 0.002 * k) & (hit < 0.002 * k + 0.001)] = x
+    for k, x in enumerate((np.nan, np.inf, -1.0, -2.0 ** -149)):
+        c.v[(hit > 0.1 + 0.002 * k) & (hit < 0.101 + 0.002 * k)] = x
+    for k, x in enumerate((0.0, -0.0, 2.0 ** -149, 2.0 ** -130)):
+        c.v[(hit > 0.2 + 0.1 * k) & (hit < 0.25 + 0.1 * k)] = x
+        c.m[(hit > 0.2 + 0.1 * k) & (hit < 0.25 + 0.1 * k)] = -x
+    st = c.reset()
+    n_scales = st.plan.adamw_n_scales
+    m8, r8, sc = (torch.full((k,), 77, dtype=torch.uint8, device=DEV) for k in (c.S, c.S, 2 * n_scales))
+    Z.zero_adamw8_load(st.plan, st.m, st.v, m8, r8, sc)
+    inside = c.own >= 0
+    with np.errstate(invalid="ignore"):
+        root = np.sqrt(c.v)
+    wm, bm = R.encode(c.m, c.idx, inside, n_scales, "m")
+    wr, br = R.encode(root, c.idx, inside, n_scales, "r")
+    assert (bm == 255).any() and (br == 255).any()
+    want = np.stack([np.where(bm < 0, 77, bm), np.where(br < 0, 77, br)], 1).reshape(-1)
+    assert np.array_equal(host(sc), want.astype(np.uint8))
+    assert np.array_equal(host(m8), np.where(inside, wm, 77))
+    assert np.array_equal(host(r8), np.where(inside, wr, 77))
+    m16, r16 = (torch.zeros(c.S, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    Z.zero_adamw8_unload(st.plan, m8, r8, sc, m16, r16)
+    bad_m, bad_r = (inside & (b[np.minimum(c.idx, n_scales - 1)] == 255) for b in (bm, br))
+    assert np.array_equal(np.isnan(host(m16.float())), bad_m) and np.array_equal(np.isnan(host(r16.float())), bad_r)
