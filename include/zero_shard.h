@@ -488,7 +488,7 @@ zero_status zero_adamw_get_sizes(const zero_plan* plan, zero_adamw_sizes* out);
 typedef struct zero_adamw_hparams {
     double lr;                            /* >= 0                                          */
     double beta1, beta2;                  /* in [0, 1)                                     */
-    double eps;                           /* >= 2^-126, finite in fp32                      */
+    double eps;                           /* >= 2^-126, finite in fp32                     */
     double weight_decay;                  /* >= 0                                          */
     double grad_scale;                    /* as zero_adam_hparams                          */
     double max_norm;                      /* >= 0; 0 = no clipping; > 0 needs grad_sumsq   */
@@ -548,8 +548,9 @@ zero_status zero_adamw_step(const zero_plan* plan, const float* d_g32, float* d_
  * inputs give equal bits.  A block whose new m (r) is not finite everywhere -- a gradient
  * that is not, or whose square passes fp32's range (|g| above 1.8e19), in a step that no flag
  * skips -- gets scale byte 255 and codes 0, and all of it reads as NaN from then on.  The variance
- * does not leave fp32's range below: r is right down to the least code, 2^-113.  States of dead parameters, row gaps and
- * skipped steps stay as they were.  Each state element takes 2 bytes and 1/64 instead of 8.
+ * does not leave fp32's range below: r is right down to the least code, 2^-113.  States of dead
+ * parameters, row gaps and skipped steps stay as they were.  Each state element takes 2 bytes and 1/64
+ * instead of 8.
  *   d_m8, d_r8   device uint8[shard_numel], 16-byte aligned
  *   d_scales     device uint8[2 * n_scales], 16-byte aligned; entries that no block has are not used
  * Other arguments and errors as zero_adamw_step. */

@@ -6,8 +6,8 @@
 // overflow flag (and sets it where the sum of squares of all ranks is not finite), advances the live parameters' step counts and forms every scalar of the step in
 // double: the clip coefficient from the sum of squares, the gradient multiplier, the rate from
 // the schedule's factor, and per parameter the step size, the bias correction and the decay.
-// adamw_kernel then streams the shard: 16 bytes in and 14 out per element, bound by memory (6.35 TB/s on
-// the GPT-2 list at Nd = 8, 920 us; 6.0 TB/s on the 7.5B list at Nd = 64, 578 us, on MI355X; counters:
+// adamw_kernel then streams the shard: 16 bytes in and 14 out per element, bound by memory (6.2 TB/s on
+// the GPT-2 list at Nd = 8, 948 us; 6.0 TB/s on the 7.5B list at Nd = 64, 580 us, on MI355X; counters:
 // 5.86 GB moved of 5.84 needed).
 #include <cmath>
 
@@ -87,7 +87,7 @@ struct AdamWArgs {
 };
 
 // From this many tiles on, the kernel reserves LDS for two blocks per CU (two_blocks_lds).  Measured
-// on MI355X, reserved against not: 22.9 us against 18.4 on the ragged list's 1270 tiles,
+// on MI355X, calls among others, reserved against not: 22.9 us against 18.4 on the ragged list's 1270 tiles,
 // 46 both at 4.0K tiles of the GPT-2 list, 81 against 80 at 7.9K, 159 against 165 at 15.8K, 312
 // against 320 at 31.7K, 919 against 925 at 95K.
 constexpr int64_t kManyTiles = 12 * 1024;

@@ -6,12 +6,13 @@
 // A wavefront takes a run of 256 columns, 4 a lane, so that a block's largest magnitude is one
 // reduction inside the wavefront and every array is read and written in whole lines.
 //
-// Measured on MI355X: 547 us for the GPT-2 list's 194.7M elements at Nd = 8 (6.4 TB/s; counters: 1.97
-// GB fetched and 1.57 written against 1.95 and 1.56 that the step needs), 354 us for the 7.5B list's
-// 116.6M at Nd = 64 (5.9 TB/s).  The arithmetic is 63 vector instructions an element, about 60% of
-// that time; at 95, with the conversions, the root and the quotient written out, it took 625 us.
-// More wavefronts than the 80 registers allow (forced to 64 registers) or fewer are slower: 611 us
-// at eight per SIMD, 556 at four, 594 at three.
+// Measured on MI355X: 569 us for the GPT-2 list's 194.7M elements at Nd = 8 (6.2 TB/s; counters: 1.97
+// GB fetched and 1.57 written against 1.95 and 1.56 that the step needs), 360 us for the 7.5B list's
+// 116.6M at Nd = 64 (5.8 TB/s).  The arithmetic is 74 vector instructions an element.  11 of them keep
+// the smallest roots, the quotient's last bit and parameters that are -0 or infinite right; without
+// those it took 547 and 351 us.  With the conversions, the root and the quotient written out it was 95
+// instructions and 625 us.  More wavefronts than the 80 registers allow (forced to 64 registers) or
+// fewer are slower, measured at 547 us: 611 at eight per SIMD, 556 at four, 594 at three.
 #include <cmath>
 
 #include "zs_adamw.h"
